@@ -21,6 +21,7 @@ __all__ = [
     "rope_table", "cast_fp8_per_head", "joint_attention", "BlockWeights", "prepare_block_weights",
     "DitShape", "DitWeights", "dit_step", "dit_workspace_size",
     "joint_block_forward", "block_workspace_size", "device_status", "scales_mma_to_linear",
+    "FP8Block", "quantize_fp8_block", "gemm_fp8_block", "rope_axes", "layer_norm_forward", "layer_norm_backward",
 ]
 
 KL_OK = 0
@@ -93,6 +94,18 @@ class _DitViews(ctypes.Structure):
                 ("head_gs", ctypes.c_size_t), ("velocity", ctypes.c_size_t)]
 
 
+class _FP8Tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class _RopeArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("pos_type", ctypes.c_int), ("pos_shared", ctypes.c_int), ("flags", ctypes.c_int),
+                ("naxes", ctypes.c_int), ("sections", ctypes.c_int64 * 4), ("batch", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("heads", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3), ("theta", ctypes.c_double)]
+
+
 class _DitCacheHeader(ctypes.Structure):
     _fields_ = [("num", ctypes.c_double), ("den", ctypes.c_double), ("diff", ctypes.c_float), ("hit", ctypes.c_int),
                 ("has_ref", ctypes.c_int), ("hits", ctypes.c_int), ("steps", ctypes.c_int)]
@@ -142,6 +155,16 @@ _SIGS = {
     "kl_dit_cache_reset": ([_VP, _VP], _I),
     "kl_dit_step_cached": ([ctypes.POINTER(_DitShape), ctypes.POINTER(_DitWeights), ctypes.POINTER(_DitStepIO),
                             ctypes.c_float, _VP, _SZ, _VP, _SZ, _VP], _I),
+    "kl_fp8_scales_bytes": ([_I64, _I64, _I], _SZ),
+    "kl_quantize_fp8_block": ([_VP, _I, _I64, _I64, _I64, _VP, _I64, _VP, _I, _VP], _I),
+    "kl_gemm_fp8_block": ([ctypes.POINTER(_FP8Tensor), ctypes.POINTER(_FP8Tensor), _I64, _I64, _I64, _VP, _I, _I64,
+                           _I, _VP], _I),
+    "kl_rope_axes": ([ctypes.POINTER(_RopeArgs), _VP], _I),
+    "kl_layer_norm_forward": ([_VP, _I, _I64, _I64, _I64, _VP, _VP, _I, _I64, ctypes.c_float, _I, _VP, _I64, _VP, _VP,
+                               _VP], _I),
+    "kl_layer_norm_backward_workspace_size": ([_I, _I64, _I64, _I64], _SZ),
+    "kl_layer_norm_backward": ([_VP, _I64, _VP, _I64, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I, _VP, _I64, _VP,
+                                _VP, _VP, _SZ, _VP], _I),
 }
 
 
@@ -650,6 +673,230 @@ def dit_step_cached(shape, weights, cache, threshold, latent, text, mod_mode, mo
                                     cache.buf.data_ptr(), cache.buf.numel(), workspace.data_ptr(), workspace.numel(),
                                     _stream()), "kl_dit_step_cached")
     return latent
+
+
+# ------------------------------------------- the eight-bit projection path
+# These calls run on the current stream of their tensors' device, whichever
+# device is current, and allocate outputs and scratch per call.
+KL_FP8_TILE, KL_FP8_TRANSPOSE = 16, 32
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+_POS_TYPE = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
+FP8_GEMM_KERNELS = {"auto": 0, "pair_256x256": 1, "pair_256x128": 2, "split": 3}
+
+
+def _call(device, name, *args):
+    """Call an entry point whose last argument is the stream, on ``device``."""
+    fn = getattr(lib(), name)
+    if device.index is None or device.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if status != KL_OK:
+        raise KLError(status, name)
+
+
+def _need_on(t, device, dtypes, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected a CUDA tensor of {' / '.join(str(d) for d in dtypes)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
+
+
+def _rows(t, name):
+    """(rows, cols, row stride) of ``t`` [..., cols] as a matrix whose rows lie
+    at one stride; raises if it is not one (no copy is made)."""
+    if t.dim() < 1 or t.numel() == 0:
+        raise ValueError(f"{name}: expected a tensor [..., cols] that is not empty")
+    if t.is_contiguous():
+        cols = t.shape[-1]
+        return t.numel() // cols, cols, cols
+    cols = t.shape[-1]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be consecutive")
+    rows, ld = 1, cols
+    for n, st in reversed(list(zip(t.shape[:-1], t.stride()[:-1]))):
+        if n == 1:
+            continue
+        if rows == 1:
+            ld = st
+        elif st != rows * ld:
+            raise ValueError(f"{name}: rows must lie at one stride")
+        rows *= n
+    if ld < cols:
+        raise ValueError(f"{name}: rows must not overlap")
+    return rows, cols, ld
+
+
+@dataclass
+class FP8Block:
+    """E4M3 codes uint8 [rows, ld] (ld: cols up to a multiple of 16) and E8M0
+    scale bytes, one per block of 128 columns (``block`` "row") or per 128 x 128
+    tile ("tile"); layout "mma" (the product's) or "linear"."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    cols: int
+    layout: str = "mma"
+    block: str = "row"
+
+    def abi(self):
+        return _FP8Tensor(self.codes.data_ptr(), self.scales.data_ptr(), self.codes.stride(0))
+
+
+def quantize_fp8_block(x, block="row", transpose=False, layout="mma"):
+    """kl_quantize_fp8_block of ``x`` [..., cols] (bf16, fp16 or fp32 CUDA
+    tensor; leading dimensions are rows), or of its transpose: an FP8Block."""
+    _need_on(x, None, _DTYPE, "x")
+    if block not in ("row", "tile") or layout not in ("mma", "linear"):
+        raise ValueError('block: "row" or "tile"; layout: "mma" or "linear"')
+    R, C, ld = _rows(x, "x")
+    rows, cols = (C, R) if transpose else (R, C)
+    flags = (KL_SCALE_MMA if layout == "mma" else 0) | (KL_FP8_TILE if block == "tile" else 0) | (
+        KL_FP8_TRANSPOSE if transpose else 0)
+    codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=x.device)
+    scales = torch.empty(lib().kl_fp8_scales_bytes(rows, cols, flags), dtype=torch.uint8, device=x.device)
+    _call(x.device, "kl_quantize_fp8_block", x.data_ptr(), _DTYPE[x.dtype], R, C, ld, codes.data_ptr(),
+          codes.stride(0), scales.data_ptr(), flags)
+    if layout == "linear":
+        scales = scales.view(-1, (cols + 127) // 128)
+    return FP8Block(codes, scales, rows, cols, layout, block)
+
+
+def gemm_fp8_block(A, W, out=None, out_dtype=torch.bfloat16, kernel="auto"):
+    """kl_gemm_fp8_block: A W^T of two FP8Blocks [M, K] and [N, K] in the "mma"
+    layout, as bf16 or fp32 [M, N].  ``out`` (optional): a 2-D tensor to write,
+    its rows at any stride.  ``kernel``: "auto" or one of FP8_GEMM_KERNELS."""
+    if A.layout != "mma" or W.layout != "mma" or A.cols != W.cols:
+        raise ValueError("operands must share K and use the MMA scale layout")
+    device = A.codes.device
+    for q, n in ((A, "A"), (W, "W")):
+        _need_on(q.codes, device, (torch.uint8,), f"{n}.codes")
+        _need_on(q.scales, device, (torch.uint8,), f"{n}.scales")
+        if q.codes.dim() != 2 or q.codes.shape[0] < q.rows or q.codes.shape[1] < q.cols or q.codes.stride(1) != 1:
+            raise ValueError(f"{n}.codes: expected [rows, >= cols] with consecutive columns")
+        if not q.scales.is_contiguous() or q.scales.numel() < (q.rows + 127) // 128 * ((q.cols + 511) // 512) * 512:
+            raise ValueError(f"{n}.scales: too small for [{q.rows}, {q.cols}]")
+    M, N, K = A.rows, W.rows, A.cols
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=device)
+    else:
+        _need_on(out, device, (torch.bfloat16, torch.float32), "out")
+        if tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
+            raise ValueError(f"out: expected [{M}, {N}] with consecutive columns")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype: bfloat16 or float32")
+    a, w = A.abi(), W.abi()
+    _call(device, "kl_gemm_fp8_block", ctypes.byref(a), ctypes.byref(w), M, N, K, out.data_ptr(),
+          KL_OUT_F32 if out.dtype == torch.float32 else KL_OUT_BF16, max(out.stride(0), N), FP8_GEMM_KERNELS[kernel])
+    return out
+
+
+def rope_axes(x, pos, sections, theta=10000.0, pairing="interleaved", ladder="axis", inverse=False, out=None):
+    """kl_rope_axes: rotary positions on ``x`` [tokens, heads, dim] or [batch,
+    tokens, heads, dim] (dims consecutive, any other strides).  ``pos``: int32,
+    int64 or fp32 [tokens, axes], or [batch, tokens, axes]; ``sections``: pairs
+    per axis.  ``pairing``: "interleaved" (2j, 2j + 1) or "half" (j, j + P);
+    ``ladder``: "axis" or "shared".  ``inverse`` turns back: the gradient.
+    ``out``: a tensor of x's shape and type, or ``x`` itself (in place)."""
+    _need_on(x, None, _DTYPE, "x")
+    _need_on(pos, x.device, _POS_TYPE, "pos")
+    if x.dim() not in (3, 4) or x.numel() == 0 or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        raise ValueError("x: expected [tokens, heads, dim] or [batch, tokens, heads, dim], dims consecutive")
+    if pairing not in ("interleaved", "half") or ladder not in ("axis", "shared"):
+        raise ValueError('pairing: "interleaved" or "half"; ladder: "axis" or "shared"')
+    batch = x.shape[0] if x.dim() == 4 else 1
+    tokens, heads, dim = x.shape[-3:]
+    naxes = len(sections)
+    shape = tuple(pos.shape)
+    shared = shape == (tokens, naxes)
+    if not 1 <= naxes <= 4 or not (shared or (x.dim() == 4 and shape == (batch, tokens, naxes))):
+        raise ValueError(f"pos: expected [{tokens}, {naxes}] or [{batch}, {tokens}, {naxes}], 1 to 4 axes")
+    pos = pos.contiguous()
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _need_on(out, x.device, (x.dtype,), "out")
+        if out.shape != x.shape or (dim > 1 and out.stride(-1) != 1) or any(
+                n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
+            raise ValueError("out: expected x's shape, dims consecutive, no broadcast dimensions")
+
+    def strides(t):
+        return t.stride()[:3] if t.dim() == 4 else (0, *t.stride()[:2])
+
+    flags = (pairing == "half") | (ladder == "shared") << 1 | bool(inverse) << 2
+    args = _RopeArgs(x.data_ptr(), out.data_ptr(), pos.data_ptr(), _DTYPE[x.dtype], _POS_TYPE[pos.dtype], shared,
+                     flags, naxes, (ctypes.c_int64 * 4)(*sections), batch, tokens, heads, dim,
+                     (ctypes.c_int64 * 3)(*strides(x)), (ctypes.c_int64 * 3)(*strides(out)), theta)
+    _call(x.device, "kl_rope_axes", ctypes.byref(args))
+    return out
+
+
+def _ln_params(rows, cols, device, params, groups):
+    """(groups, dtype code) of gain / bias tensors [cols] or [groups, cols]."""
+    dtype = None
+    for t, n in params:
+        if t is None:
+            continue
+        _need_on(t, device, _DTYPE, n)
+        if not t.is_contiguous() or t.dim() not in (1, 2) or t.shape[-1] != cols:
+            raise ValueError(f"{n}: expected a contiguous [{cols}] or [groups, {cols}] tensor")
+        g = t.shape[0] if t.dim() == 2 else 1
+        if groups is not None and g != groups:
+            raise ValueError(f"{n}: {g} groups, expected {groups}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError("gain and bias must have one type")
+        groups, dtype = g, t.dtype
+    groups = 1 if groups is None else groups
+    if groups < 1 or rows % groups:
+        raise ValueError(f"{groups} groups do not divide {rows} rows")
+    return groups, _DTYPE[dtype] if dtype is not None else 1
+
+
+def layer_norm_forward(x, gain=None, bias=None, modulate=False, eps=1e-6):
+    """kl_layer_norm_forward over the last dimension of ``x`` [..., cols]:
+    (y, mean, rstd), mean and rstd fp32 [rows].  ``gain`` / ``bias``: [cols], or
+    [groups, cols] with the rows divided evenly among the groups; ``modulate``:
+    the factor is 1 + gain (adaLN)."""
+    _need_on(x, None, _DTYPE, "x")
+    R, C, ld = _rows(x, "x")
+    groups, ptype = _ln_params(R, C, x.device, ((gain, "gain"), (bias, "bias")), None)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    stats = torch.empty((2, R), dtype=torch.float32, device=x.device)
+    _call(x.device, "kl_layer_norm_forward", x.data_ptr(), _DTYPE[x.dtype], R, C, ld, _ptr(gain), _ptr(bias), ptype,
+          groups, eps, 1 if modulate else 0, y.data_ptr(), C, stats.data_ptr(), stats.data_ptr() + 4 * R)
+    return y, stats[0], stats[1]
+
+
+def layer_norm_backward(dy, x, mean, rstd, gain=None, modulate=False, groups=None, param_grads=True):
+    """kl_layer_norm_backward: (dx, dgain, dbias) from the forward's x, mean and
+    rstd; dgain and dbias fp32 [groups, cols] (None without ``param_grads``).
+    ``groups``: the gain's number of rows, or how many groups' sums are wanted
+    when there is no gain."""
+    _need_on(x, None, _DTYPE, "x")
+    _need_on(dy, x.device, (x.dtype,), "dy")
+    if dy.shape != x.shape:
+        raise ValueError("dy and x must have one shape")
+    R, C, ld = _rows(x, "x")
+    lddy = _rows(dy, "dy")[2]
+    for t, n in ((mean, "mean"), (rstd, "rstd")):
+        _need_on(t, x.device, (torch.float32,), n)
+        if t.numel() != R or not t.is_contiguous():
+            raise ValueError(f"{n}: expected contiguous fp32 [{R}]")
+    groups, ptype = _ln_params(R, C, x.device, ((gain, "gain"),), groups)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dgain = dbias = ws = None
+    nbytes = 0
+    if param_grads:
+        sums = torch.empty((2, groups, C), dtype=torch.float32, device=x.device)
+        dgain, dbias = sums[0], sums[1]
+        nbytes = lib().kl_layer_norm_backward_workspace_size(_DTYPE[x.dtype], R, C, groups)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    _call(x.device, "kl_layer_norm_backward", dy.data_ptr(), lddy, x.data_ptr(), ld, _DTYPE[x.dtype], R, C,
+          mean.data_ptr(), rstd.data_ptr(), _ptr(gain), ptype, groups, 1 if modulate else 0, dx.data_ptr(), C,
+          _ptr(dgain), _ptr(dbias), _ptr(ws), nbytes)
+    return dx, dgain, dbias
 
 
 def device_status(clear=True):

@@ -29,6 +29,27 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
+// launch_pdl with clusters of `cluster` CTAs along x
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned cluster, size_t smem,
+                                      cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
 // HBM-bound kernels (kl_quant.cu)
 cudaError_t launch_amax_bf16(const void* x, int64_t n, float* amax, cudaStream_t s);
 cudaError_t launch_quantize(const void* x, int64_t rows, int64_t cols, void* codes, void* scales, float* gs_io,
@@ -66,6 +87,22 @@ struct GemmArgs {
   int force_bn;   // 0 = heuristic; 128 / 256 one-CTA tiles, 384 / 512 2-SM pair tiles 256 x 128 / 256 x 256
 };
 cudaError_t launch_gemm_nvfp4(const GemmArgs& a, cudaStream_t s);
+
+// tcgen05 FP8 product with a scale per block of 128 (kl_fp8_gemm.cu)
+struct GemmFp8Args {
+  const void* a_codes;
+  const void* a_scales;
+  int64_t lda, rows_a;
+  const void* b_codes;
+  const void* b_scales;
+  int64_t ldb, rows_b;
+  int64_t K;
+  void* out;      // [rows_a, rows_b], row stride ldo elements
+  int64_t ldo;
+  int out_f32;
+  int force;      // KL_FP8_GEMM_*
+};
+cudaError_t launch_gemm_fp8(const GemmFp8Args& a, cudaStream_t s);
 
 // tcgen05 flash attention (kl_attn.cu)
 struct AttnArgs {

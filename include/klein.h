@@ -613,6 +613,147 @@ kl_status kl_dit_step_cached(const kl_dit_shape* shape, const kl_dit_weights* w,
                              float threshold, void* cache, size_t cache_bytes, void* workspace, size_t ws_bytes,
                              void* stream);
 
+/* ------------------------------------------------------------------------
+ * The projection path at eight bits, on any token grid, with gradients.
+ *
+ * The block above encodes its operands as NVFP4; the entry points below are
+ * the same steps for layers kept at eight bits, for tokens whose positions
+ * are not the block's own grid (video, resampled grids), and for training:
+ * an FP8 encode and product, rotary positions applied to a tensor, and
+ * LayerNorm with its backward pass.  Rows have strides (ld, in elements), any
+ * number of columns, and bf16, fp16 or fp32 elements; pointers need only the
+ * alignment of their element type unless stated.  None of these calls uses
+ * a workspace except kl_layer_norm_backward; none keeps anything between calls.
+ * ---------------------------------------------------------------------- */
+#define KL_BF16 0
+#define KL_F32 1
+#define KL_F16 2
+
+/*
+ * kl_quantize_fp8_block -- E4M3 codes of x [rows, cols] with one power-of-two
+ * scale per block of 128: 128 consecutive columns of a row, or a 128 x 128
+ * tile with KL_FP8_TILE; with KL_FP8_TRANSPOSE of x^T [cols, rows] (its rows
+ * and columns are meant from here on).  Per block: the scale is 2^e, e the least
+ * integer with amax <= 448 * 2^e, in [-127, 127] (0 if amax is 0); code =
+ * e4m3_rne(x * 2^-e), which never saturates.  A block with a NaN or an
+ * infinity gets the scale NaN and NaN codes, and KL_ERR_NONFINITE is recorded.
+ * codes: uint8 [rows, ldc], 16-byte aligned, ldc a multiple of 16; columns up
+ *   to the next multiple of 16 are written (zeros past the last), those beyond
+ *   are left as they are.
+ * scales: E8M0 bytes (e + 127; 255 = NaN), kl_fp8_scales_bytes bytes, 4-byte
+ *   aligned.  KL_SCALE_LINEAR: [rows, blocks], or [ceil(rows/128), blocks]
+ *   with KL_FP8_TILE, blocks = ceil(cols/128).  KL_SCALE_MMA (the product's
+ *   layout): 512-byte atoms, one per (128 rows, 4 blocks), atom index (row/128)
+ *   * ceil(blocks/4) + block/4, byte (row%32)*16 + ((row/32)%4)*4 + block%4; a
+ *   tile's scale stands at each of its 128 rows; bytes past the last row or
+ *   block are 0.
+ */
+#define KL_FP8_TILE 16
+#define KL_FP8_TRANSPOSE 32
+#define KL_FP8_MAX_DIM 0x7FFFFFFF /* rows, cols, and 128 x 128 tiles */
+size_t kl_fp8_scales_bytes(int64_t rows, int64_t cols, int flags); /* of the encoded matrix */
+kl_status kl_quantize_fp8_block(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, void* codes,
+                                int64_t ldc, void* scales, int flags, void* stream);
+
+/* An FP8 operand of the product: codes [rows, K] with row stride ld bytes (a
+ * multiple of 16), scales in the KL_SCALE_MMA layout above; both 16-byte aligned. */
+typedef struct kl_fp8_tensor {
+  const void* codes;
+  const void* scales;
+  int64_t ld;
+} kl_fp8_tensor;
+
+/*
+ * kl_gemm_fp8_block -- out[m, n] = sum_k dec(A)[m, k] dec(W)[n, k], both
+ * operands K-major ("y = x W^T"), any M, N, K >= 1, out bf16 or fp32 with row
+ * stride ldo elements.  Products are exact, sums fp32 in the tensor core.  The
+ * gradients of y = x W^T are the same call on transposed encodings:
+ *   dx = dy . (W^T)^T     A = dy by rows, W = W with KL_FP8_TRANSPOSE
+ *   dW = dy^T . (x^T)^T   A = dy with KL_FP8_TRANSPOSE, W = x with KL_FP8_TRANSPOSE
+ * kernel: KL_FP8_GEMM_AUTO, or a forced variant (tests, tuning).  The split
+ * variant divides K over a cluster; the same call gives the same bits every
+ * time, but the two kernels add in different orders.
+ * An operand row or block whose scale is NaN makes its outputs NaN.
+ */
+#define KL_FP8_GEMM_AUTO 0
+#define KL_FP8_GEMM_PAIR_256x256 1 /* 2-SM pair tiles */
+#define KL_FP8_GEMM_PAIR_256x128 2
+#define KL_FP8_GEMM_SPLIT 3        /* 128 weight rows x 16 to 128 tokens, K over a cluster */
+#define KL_FP8_GEMM_MAX 0x40000000 /* M, N, K */
+kl_status kl_gemm_fp8_block(const kl_fp8_tensor* A, const kl_fp8_tensor* W, int64_t M, int64_t N, int64_t K,
+                            void* out, int out_dtype, int64_t ldo, int kernel, void* stream);
+
+/*
+ * kl_rope_axes -- rotary positions with up to four axes (for instance time,
+ * height, width) on x [batch, tokens, heads, dim], into out.  The first 2P
+ * dims of a head are P pairs, dealt to the axes in order, sections[a] pairs to
+ * axis a; pair j of axis a turns (x0, x1) -> (x0 c - x1 s, x0 s + x1 c) by
+ *   pos[b, t, a] * theta^(-u / sections[a]), u the pair's index in its section
+ *   (with KL_ROPE_LADDER_SHARED: pos[b, t, a] * theta^(-j / P)).
+ * A pair is dims (2j, 2j+1), or (j, j + P) with KL_ROPE_HALF.  Dims past 2P are
+ * copied.  KL_ROPE_INVERSE turns by the negative angle: the inverse, and the
+ * gradient with respect to x.  With sections (16, 24, 24), dim 128 and pos =
+ * (frame, row, column) the angles are kl_rope_table's for image tokens.
+ * Angles are fp64 until they are reduced by whole turns; cos, sin and the
+ * rotation are fp32.
+ * Strides (batch, token, head) are in elements, dims are consecutive; dim <=
+ * 512.  pos: int32, int64 or fp32 [batch, tokens, naxes] consecutive, or
+ * [tokens, naxes] for every batch with pos_shared.  out may be x itself with
+ * the same strides (in place); otherwise they must not overlap.
+ */
+#define KL_ROPE_MAX_AXES 4
+#define KL_ROPE_HALF 1
+#define KL_ROPE_LADDER_SHARED 2
+#define KL_ROPE_INVERSE 4
+#define KL_POS_I32 0
+#define KL_POS_I64 1
+#define KL_POS_F32 2
+typedef struct kl_rope_args {
+  const void* x;
+  void* out;
+  const void* pos;
+  int dtype;      /* KL_BF16, KL_F32, KL_F16 of x and out */
+  int pos_type;   /* KL_POS_* */
+  int pos_shared; /* non-zero: pos is [tokens, naxes] */
+  int flags;      /* KL_ROPE_* */
+  int naxes;
+  int64_t sections[KL_ROPE_MAX_AXES];
+  int64_t batch, tokens, heads, dim;
+  int64_t x_stride[3];
+  int64_t out_stride[3];
+  double theta;   /* > 1 */
+} kl_rope_args;
+kl_status kl_rope_axes(const kl_rope_args* args, void* stream);
+
+/*
+ * kl_layer_norm_forward -- y = (x - mean) * rstd * g + b over the columns of
+ * each row: mean and biased variance of the row, rstd = 1 / sqrt(var + eps);
+ * g = gain, 1 + gain with KL_LN_MODULATE, 1 without (NULL); b = bias or 0.
+ * gain / bias [groups, cols] of param_dtype, consecutive: row r uses group
+ * r / (rows / groups) (one modulation per image of a batch; groups = 1: shared
+ * by all rows; groups must divide rows).  mean, rstd fp32 [rows], NULL if not
+ * wanted.  eps >= 0.
+ *
+ * kl_layer_norm_backward -- from dy, x and the forward's mean and rstd:
+ *   dx = rstd * (h - mean_c(h) - xhat * mean_c(h * xhat)), h = dy * g;
+ *   dgain[group, c] = sum of dy * xhat, dbias = sum of dy over the group's
+ *   rows, fp32 [groups, cols], both or neither (NULL: dx alone, no workspace).
+ * The sums are taken in a fixed order.  Outputs must not overlap inputs.
+ * workspace: >= kl_layer_norm_backward_workspace_size bytes, 16-byte aligned.
+ */
+#define KL_LN_MODULATE 1
+#define KL_LN_MAX_ROWS 0x7FFFFFFF
+#define KL_LN_MAX_COLS 0x1000000
+#define KL_LN_MAX_GROUPS 65535
+kl_status kl_layer_norm_forward(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, const void* gain,
+                                const void* bias, int param_dtype, int64_t groups, float eps, int flags, void* y,
+                                int64_t ldy, float* mean, float* rstd, void* stream);
+size_t kl_layer_norm_backward_workspace_size(int dtype, int64_t rows, int64_t cols, int64_t groups);
+kl_status kl_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, int dtype, int64_t rows,
+                                 int64_t cols, const float* mean, const float* rstd, const void* gain, int param_dtype,
+                                 int64_t groups, int flags, void* dx, int64_t lddx, float* dgain, float* dbias,
+                                 void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
