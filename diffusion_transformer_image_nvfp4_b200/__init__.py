@@ -681,17 +681,25 @@ def dit_step_cached(shape, weights, cache, threshold, latent, text, mod_mode, mo
 KL_FP8_TILE, KL_FP8_TRANSPOSE = 16, 32
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 _POS_TYPE = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
+_OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+_U8, _F32 = (torch.uint8,), (torch.float32,)
+_PAIRING, _LADDER = {"interleaved": 0, "half": 1}, {"axis": 0, "shared": 2}
+_I64x3, _I64x4 = ctypes.c_int64 * 3, ctypes.c_int64 * 4
 FP8_GEMM_KERNELS = {"auto": 0, "pair_256x256": 1, "pair_256x128": 2, "split": 3}
 
 
+# The small calls are bound by this file's own work (a launch is about 4 us of
+# the CPU, torch.empty 1.3 to 2.3, a torch.cuda.Stream object 3), so it asks
+# for the raw stream and makes its tensors the cheapest way.
 def _call(device, name, *args):
-    """Call an entry point whose last argument is the stream, on ``device``."""
-    fn = getattr(lib(), name)
-    if device.index is None or device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    """Call an entry point whose last argument is the stream, on ``device`` (a
+    tensor's: its index is known)."""
+    fn, index = getattr(_LIB or lib(), name), device.index
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != KL_OK:
         raise KLError(status, name)
 
@@ -706,16 +714,17 @@ def _need_on(t, device, dtypes, name):
 def _rows(t, name):
     """(rows, cols, row stride) of ``t`` [..., cols] as a matrix whose rows lie
     at one stride; raises if it is not one (no copy is made)."""
-    if t.dim() < 1 or t.numel() == 0:
+    shape = t.shape
+    n = t.numel()
+    if not shape or n == 0:
         raise ValueError(f"{name}: expected a tensor [..., cols] that is not empty")
+    cols = shape[-1]
     if t.is_contiguous():
-        cols = t.shape[-1]
-        return t.numel() // cols, cols, cols
-    cols = t.shape[-1]
+        return n // cols, cols, cols
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be consecutive")
     rows, ld = 1, cols
-    for n, st in reversed(list(zip(t.shape[:-1], t.stride()[:-1]))):
+    for n, st in reversed(list(zip(shape[:-1], t.stride()[:-1]))):
         if n == 1:
             continue
         if rows == 1:
@@ -726,6 +735,11 @@ def _rows(t, name):
     if ld < cols:
         raise ValueError(f"{name}: rows must not overlap")
     return rows, cols, ld
+
+
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 @dataclass
@@ -741,8 +755,17 @@ class FP8Block:
     layout: str = "mma"
     block: str = "row"
 
-    def abi(self):
-        return _FP8Tensor(self.codes.data_ptr(), self.scales.data_ptr(), self.codes.stride(0))
+    def abi(self, device, name):
+        """The checked operand of kl_gemm_fp8_block on ``device``."""
+        codes, scales, rows, cols = self.codes, self.scales, self.rows, self.cols
+        _need_on(codes, device, _U8, name)
+        _need_on(scales, device, _U8, name)
+        shape, ld = codes.shape, codes.stride()
+        if len(shape) != 2 or shape[0] < rows or shape[1] < cols or ld[1] != 1:
+            raise ValueError(f"{name}.codes: expected [rows, >= cols] with consecutive columns")
+        if not scales.is_contiguous() or scales.numel() < (rows + 127) // 128 * ((cols + 511) // 512) * 512:
+            raise ValueError(f"{name}.scales: too small for [{rows}, {cols}]")
+        return _FP8Tensor(codes.data_ptr(), scales.data_ptr(), ld[0])
 
 
 def quantize_fp8_block(x, block="row", transpose=False, layout="mma"):
@@ -755,12 +778,16 @@ def quantize_fp8_block(x, block="row", transpose=False, layout="mma"):
     rows, cols = (C, R) if transpose else (R, C)
     flags = (KL_SCALE_MMA if layout == "mma" else 0) | (KL_FP8_TILE if block == "tile" else 0) | (
         KL_FP8_TRANSPOSE if transpose else 0)
-    codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(lib().kl_fp8_scales_bytes(rows, cols, flags), dtype=torch.uint8, device=x.device)
-    _call(x.device, "kl_quantize_fp8_block", x.data_ptr(), _DTYPE[x.dtype], R, C, ld, codes.data_ptr(),
-          codes.stride(0), scales.data_ptr(), flags)
-    if layout == "linear":
-        scales = scales.view(-1, (cols + 127) // 128)
+    ldc, blocks = (cols + 15) // 16 * 16, (cols + 127) // 128
+    device = x.device
+    codes = torch.empty((rows, ldc), dtype=torch.uint8, device=device)
+    if layout == "mma":
+        scales = torch.empty((rows + 127) // 128 * ((blocks + 3) // 4) * 512, dtype=torch.uint8, device=device)
+    else:
+        scales = torch.empty(((rows + 127) // 128 if block == "tile" else rows, blocks), dtype=torch.uint8,
+                             device=device)
+    _call(device, "kl_quantize_fp8_block", x.data_ptr(), _DTYPE[x.dtype], R, C, ld, codes.data_ptr(), ldc,
+          scales.data_ptr(), flags)
     return FP8Block(codes, scales, rows, cols, layout, block)
 
 
@@ -771,25 +798,19 @@ def gemm_fp8_block(A, W, out=None, out_dtype=torch.bfloat16, kernel="auto"):
     if A.layout != "mma" or W.layout != "mma" or A.cols != W.cols:
         raise ValueError("operands must share K and use the MMA scale layout")
     device = A.codes.device
-    for q, n in ((A, "A"), (W, "W")):
-        _need_on(q.codes, device, (torch.uint8,), f"{n}.codes")
-        _need_on(q.scales, device, (torch.uint8,), f"{n}.scales")
-        if q.codes.dim() != 2 or q.codes.shape[0] < q.rows or q.codes.shape[1] < q.cols or q.codes.stride(1) != 1:
-            raise ValueError(f"{n}.codes: expected [rows, >= cols] with consecutive columns")
-        if not q.scales.is_contiguous() or q.scales.numel() < (q.rows + 127) // 128 * ((q.cols + 511) // 512) * 512:
-            raise ValueError(f"{n}.scales: too small for [{q.rows}, {q.cols}]")
+    a, w = A.abi(device, "A"), W.abi(device, "W")
     M, N, K = A.rows, W.rows, A.cols
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=device)
+        if out_dtype not in _OUT_TYPE:
+            raise ValueError("out_dtype: bfloat16 or float32")
+        out, ldo = torch.empty((M, N), dtype=out_dtype, device=device), N
     else:
-        _need_on(out, device, (torch.bfloat16, torch.float32), "out")
+        _need_on(out, device, _OUT_TYPE, "out")
         if tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
             raise ValueError(f"out: expected [{M}, {N}] with consecutive columns")
-    if out.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("out_dtype: bfloat16 or float32")
-    a, w = A.abi(), W.abi()
+        out_dtype, ldo = out.dtype, max(out.stride(0), N)
     _call(device, "kl_gemm_fp8_block", ctypes.byref(a), ctypes.byref(w), M, N, K, out.data_ptr(),
-          KL_OUT_F32 if out.dtype == torch.float32 else KL_OUT_BF16, max(out.stride(0), N), FP8_GEMM_KERNELS[kernel])
+          _OUT_TYPE[out_dtype], ldo, FP8_GEMM_KERNELS[kernel])
     return out
 
 
@@ -801,35 +822,35 @@ def rope_axes(x, pos, sections, theta=10000.0, pairing="interleaved", ladder="ax
     ``ladder``: "axis" or "shared".  ``inverse`` turns back: the gradient.
     ``out``: a tensor of x's shape and type, or ``x`` itself (in place)."""
     _need_on(x, None, _DTYPE, "x")
-    _need_on(pos, x.device, _POS_TYPE, "pos")
-    if x.dim() not in (3, 4) or x.numel() == 0 or (x.shape[-1] > 1 and x.stride(-1) != 1):
+    device, shape, xs = x.device, x.shape, x.stride()
+    _need_on(pos, device, _POS_TYPE, "pos")
+    if len(shape) not in (3, 4) or x.numel() == 0 or (shape[-1] > 1 and xs[-1] != 1):
         raise ValueError("x: expected [tokens, heads, dim] or [batch, tokens, heads, dim], dims consecutive")
-    if pairing not in ("interleaved", "half") or ladder not in ("axis", "shared"):
+    flags = _PAIRING.get(pairing, 8) | _LADDER.get(ladder, 8) | (4 if inverse else 0)
+    if flags & 8:
         raise ValueError('pairing: "interleaved" or "half"; ladder: "axis" or "shared"')
-    batch = x.shape[0] if x.dim() == 4 else 1
-    tokens, heads, dim = x.shape[-3:]
+    four = len(shape) == 4
+    batch = shape[0] if four else 1
+    tokens, heads, dim = shape[-3:]
     naxes = len(sections)
-    shape = tuple(pos.shape)
-    shared = shape == (tokens, naxes)
-    if not 1 <= naxes <= 4 or not (shared or (x.dim() == 4 and shape == (batch, tokens, naxes))):
+    pshape = pos.shape
+    shared = pshape == (tokens, naxes)
+    if not 1 <= naxes <= 4 or not (shared or (four and pshape == (batch, tokens, naxes))):
         raise ValueError(f"pos: expected [{tokens}, {naxes}] or [{batch}, {tokens}, {naxes}], 1 to 4 axes")
     pos = pos.contiguous()
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _like(x)
+        os = (tokens * heads * dim, heads * dim, dim)
     else:
-        _need_on(out, x.device, (x.dtype,), "out")
-        if out.shape != x.shape or (dim > 1 and out.stride(-1) != 1) or any(
-                n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
+        _need_on(out, device, (x.dtype,), "out")
+        os = out.stride()
+        if out.shape != shape or (dim > 1 and os[-1] != 1) or any(n > 1 and st == 0 for n, st in zip(shape, os)):
             raise ValueError("out: expected x's shape, dims consecutive, no broadcast dimensions")
-
-    def strides(t):
-        return t.stride()[:3] if t.dim() == 4 else (0, *t.stride()[:2])
-
-    flags = (pairing == "half") | (ladder == "shared") << 1 | bool(inverse) << 2
+        os = os[:3] if four else (0, *os[:2])
     args = _RopeArgs(x.data_ptr(), out.data_ptr(), pos.data_ptr(), _DTYPE[x.dtype], _POS_TYPE[pos.dtype], shared,
-                     flags, naxes, (ctypes.c_int64 * 4)(*sections), batch, tokens, heads, dim,
-                     (ctypes.c_int64 * 3)(*strides(x)), (ctypes.c_int64 * 3)(*strides(out)), theta)
-    _call(x.device, "kl_rope_axes", ctypes.byref(args))
+                     flags, naxes, _I64x4(*sections), batch, tokens, heads, dim,
+                     _I64x3(*(xs[:3] if four else (0, *xs[:2]))), _I64x3(*os), theta)
+    _call(device, "kl_rope_axes", ctypes.byref(args))
     return out
 
 
@@ -840,9 +861,10 @@ def _ln_params(rows, cols, device, params, groups):
         if t is None:
             continue
         _need_on(t, device, _DTYPE, n)
-        if not t.is_contiguous() or t.dim() not in (1, 2) or t.shape[-1] != cols:
+        shape = t.shape
+        if not t.is_contiguous() or len(shape) not in (1, 2) or shape[-1] != cols:
             raise ValueError(f"{n}: expected a contiguous [{cols}] or [groups, {cols}] tensor")
-        g = t.shape[0] if t.dim() == 2 else 1
+        g = shape[0] if len(shape) == 2 else 1
         if groups is not None and g != groups:
             raise ValueError(f"{n}: {g} groups, expected {groups}")
         if dtype is not None and t.dtype != dtype:
@@ -861,12 +883,14 @@ def layer_norm_forward(x, gain=None, bias=None, modulate=False, eps=1e-6):
     the factor is 1 + gain (adaLN)."""
     _need_on(x, None, _DTYPE, "x")
     R, C, ld = _rows(x, "x")
-    groups, ptype = _ln_params(R, C, x.device, ((gain, "gain"), (bias, "bias")), None)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    stats = torch.empty((2, R), dtype=torch.float32, device=x.device)
-    _call(x.device, "kl_layer_norm_forward", x.data_ptr(), _DTYPE[x.dtype], R, C, ld, _ptr(gain), _ptr(bias), ptype,
-          groups, eps, 1 if modulate else 0, y.data_ptr(), C, stats.data_ptr(), stats.data_ptr() + 4 * R)
-    return y, stats[0], stats[1]
+    dtype, device = x.dtype, x.device
+    groups, ptype = _ln_params(R, C, device, ((gain, "gain"), (bias, "bias")), None)
+    y = _like(x)
+    mean = torch.empty(R, dtype=torch.float32, device=device)
+    rstd = torch.empty_like(mean)
+    _call(device, "kl_layer_norm_forward", x.data_ptr(), _DTYPE[dtype], R, C, ld, _ptr(gain), _ptr(bias), ptype,
+          groups, eps, 1 if modulate else 0, y.data_ptr(), C, mean.data_ptr(), rstd.data_ptr())
+    return y, mean, rstd
 
 
 def layer_norm_backward(dy, x, mean, rstd, gain=None, modulate=False, groups=None, param_grads=True):
@@ -880,20 +904,22 @@ def layer_norm_backward(dy, x, mean, rstd, gain=None, modulate=False, groups=Non
         raise ValueError("dy and x must have one shape")
     R, C, ld = _rows(x, "x")
     lddy = _rows(dy, "dy")[2]
+    device = x.device
     for t, n in ((mean, "mean"), (rstd, "rstd")):
-        _need_on(t, x.device, (torch.float32,), n)
+        _need_on(t, device, _F32, n)
         if t.numel() != R or not t.is_contiguous():
             raise ValueError(f"{n}: expected contiguous fp32 [{R}]")
-    groups, ptype = _ln_params(R, C, x.device, ((gain, "gain"),), groups)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    groups, ptype = _ln_params(R, C, device, ((gain, "gain"),), groups)
+    dtype = _DTYPE[x.dtype]
+    dx = _like(x)
     dgain = dbias = ws = None
     nbytes = 0
     if param_grads:
-        sums = torch.empty((2, groups, C), dtype=torch.float32, device=x.device)
-        dgain, dbias = sums[0], sums[1]
-        nbytes = lib().kl_layer_norm_backward_workspace_size(_DTYPE[x.dtype], R, C, groups)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    _call(x.device, "kl_layer_norm_backward", dy.data_ptr(), lddy, x.data_ptr(), ld, _DTYPE[x.dtype], R, C,
+        dgain = torch.empty((groups, C), dtype=torch.float32, device=device)
+        dbias = torch.empty_like(dgain)
+        nbytes = lib().kl_layer_norm_backward_workspace_size(dtype, R, C, groups)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _call(device, "kl_layer_norm_backward", dy.data_ptr(), lddy, x.data_ptr(), ld, dtype, R, C,
           mean.data_ptr(), rstd.data_ptr(), _ptr(gain), ptype, groups, 1 if modulate else 0, dx.data_ptr(), C,
           _ptr(dgain), _ptr(dbias), _ptr(ws), nbytes)
     return dx, dgain, dbias
