@@ -118,6 +118,24 @@ def test_many_rows_and_groups(R, C, groups):
         assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("R,C,groups", [(1205, 3072, 1), (2402, 1536, 2), (5001, 512, 1), (1210, 8192, 2),
+                                        (9000, 256, 3), (1300, 4096, 1)])
+def test_staged_tiles_of_rows(R, C, groups):
+    # rows enough for every SM: tiles of rows in shared memory, the last of a group ragged
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        x, dy = _randn((R, C + 16), 1, dtype, 2.0, 1.0)[:, 16:], _randn((R, C), 2, dtype)
+        gain, bias = _params("gain", groups, C, torch.float32, 3)
+        y, mean, rstd = kl.layer_norm_forward(x, gain, bias)
+        _check_forward(y, mean, rstd, x, gain, bias, False)
+        got = kl.layer_norm_backward(dy, x, mean, rstd, gain)
+        _check_backward(got, dy, x, mean, rstd, gain, False, groups)
+        again = kl.layer_norm_backward(dy, x, mean, rstd, gain)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+        dx = kl.layer_norm_backward(dy, x, mean, rstd, gain, param_grads=False)[0]
+        assert torch.equal(dx, got[0])
+    assert kl.device_status() == "KL_OK"
+
+
 def test_strides_batches_and_alignment():
     big, dbig = _randn((30, 1000), 4, torch.bfloat16, 2.0), _randn((30, 1000), 5, torch.bfloat16)
     for cut in (lambda t: t[:, 8:520], lambda t: t[:, 3:300], lambda t: t.view(6, 5, 1000)[:, 2, :640],
