@@ -585,6 +585,26 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
 }
 // float pair from a word of two bf16
 __device__ __forceinline__ uint64_t bf16x2_to_f32x2(uint32_t w) { return pack_f32x2(bf16lo_f32(w), bf16hi_f32(w)); }
+__device__ __forceinline__ float sum_f32x2(uint64_t v) {
+  float lo, hi;
+  unpack_f32x2(v, lo, hi);
+  return lo + hi;
+}
+// one vector of V elements (16 bytes) <-> V / 2 packed pairs
+template <typename T, int V>
+__device__ __forceinline__ void unpack_vec2(const uint4& q, uint64_t (&v)[V / 2]) {
+  float f[V];
+  unpack_vec<T, V>(q, f);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) v[i] = pack_f32x2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec2(T* p, const uint64_t (&v)[V / 2]) {
+  float f[V];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) unpack_f32x2(v[i], f[2 * i], f[2 * i + 1]);
+  store_vec<T, V>(p, f);
+}
 // max |.| of the bf16 values of two words, as a word of two bf16 magnitudes:
 // for non-negative bf16 the bit patterns order like the values
 __device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t acc, uint32_t w) {

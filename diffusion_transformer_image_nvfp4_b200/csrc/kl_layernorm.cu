@@ -9,15 +9,20 @@
 //
 // mean, rstd and every sum are fp32; the variance is taken about the mean in
 // a second pass over the row in registers, so a large common offset costs
-// nothing.  A row is held in registers by the threads of one thread row
-// (blockDim.x; NV vectors of V elements each), so x (and dy) are read once:
-// both directions are bound by HBM.  CTAs with narrow rows hold several rows
-// (blockDim.y).
+// nothing.  x (and dy) are read once from memory: both directions are bound by
+// HBM, once their instructions are few enough (packed pairs, parameters staged
+// or held in registers) and their loads far enough ahead.
 //
+// Forward: a warp a row where there are rows enough, else a CTA a row.
 // Backward: a thread meets the same columns in every row of its CTA, so the
 // sums for dgain and dbias stay in its registers; CTAs walk the rows of one
 // group with a fixed stride and leave one partial row each, which a second
-// kernel adds in index order -- no atomics, the same bits every run.
+// kernel adds in a fixed order -- no atomics, the same bits every run.
+//
+// B200, bf16, device time: forward 17,408 x 3,072 38.9 us (84% of the 32.6 us its bytes
+// take at the copy's rate); backward 20,992 x 3,072 65.6 us (90% of 59), dx
+// alone 61.  Rows that no vector load suits: 5,000 x 2,047 24.7 and 25.6 us.
+
 #include <type_traits>
 
 #include "../../include/klein.h"
@@ -199,86 +204,172 @@ __global__ void __launch_bounds__(1024) ln_forward_kernel(const LnParams p) {
   }
 }
 
-// A warp a row: no barrier, and every load of the row is in flight before the
-// first sum, so a few rows a scheduler already cover the memory latency.
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(128) ln_forward_warp_kernel(const LnParams p) {
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
-  const int cols = (int)p.cols;
-  const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx;
-  uint4 q[NV];
+// Many rows: a warp a row, so no barrier; CTAs stay, for rows of one group,
+// whose factors and shifts they hold in shared memory as fp32 (read per row
+// they cost more instructions than the rest of the row's work).  Arithmetic is
+// on packed pairs.  ln_smem: [gain + plus][bias], planes of four columns of
+// every vector, so a warp's 16-byte reads are consecutive.
+template <int V>
+__device__ __forceinline__ void ln_stage_params(const LnParams& p, int64_t group, float* dst) {
+  const int cols = (int)p.cols, nvec = cols / V;
+#pragma unroll V == 1 ? 8 : 2
+  for (int j = threadIdx.x; j < nvec; j += blockDim.x) {
+    float g[V], b[V];
+    ln_factor<V>(p, group * p.cols + j * V, true, g);
+    if (p.bias) {
+      load_param<V>(p.bias, p.ptype, group * p.cols + j * V, b);
+    } else {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * 32) * V;
-    q[i] = c < cols ? load_vec<T, V>(x + c) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  // a vector is summed by itself first: short chains, small rounding errors
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float v[V];
-    unpack_vec<T, V>(q[i], v);
-    float t = v[0];
-#pragma unroll
-    for (int k = 1; k < V; ++k) t += v[k];
-    s += t;
-  }
-  const float mean = warp_sum(s) / (float)cols;
-  s = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if ((lane + i * 32) * V < cols) {
-      float v[V];
-      unpack_vec<T, V>(q[i], v);
-      float t = 0.f;
-#pragma unroll
-      for (int k = 0; k < V; ++k) t = fmaf(v[k] - mean, v[k] - mean, t);
-      s += t;
+      for (int k = 0; k < V; ++k) b[k] = 0.f;
     }
-  }
-  const float rstd = 1.0f / sqrtf(warp_sum(s) / (float)cols + p.eps);
-  if (lane == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
-  }
-  const int64_t pbase = row / p.group_rows * p.cols;
-  T* y = reinterpret_cast<T*>(p.out) + row * p.ldo;
-  // one loop per parameter type: a branch in it would scatter the unrolled
-  // code over more than the instruction cache holds
-  auto finish = [&](auto kind) {
-    constexpr int KIND = decltype(kind)::value;
+    if constexpr (V == 1) {
+      dst[j] = g[0];
+      dst[cols + j] = b[0];
+    } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * 32) * V;
-      if (c < cols) {
-        float v[V], w[V];
-        unpack_vec<T, V>(q[i], v);
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = (v[k] - mean) * rstd;
-        if (p.gain) {
-          load_param_as<KIND, V>(p.gain, pbase + c, w);
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[k] *= w[k] + p.plus;
-        }
-        if (p.bias) {
-          load_param_as<KIND, V>(p.bias, pbase + c, w);
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[k] += w[k];
-        }
-        store_vec<T, V>(y + c, v);
+      for (int h = 0; h < V / 4; ++h) {
+        *reinterpret_cast<float4*>(dst + (h * nvec + j) * 4) =
+            make_float4(g[4 * h], g[4 * h + 1], g[4 * h + 2], g[4 * h + 3]);
+        *reinterpret_cast<float4*>(dst + cols + (h * nvec + j) * 4) =
+            make_float4(b[4 * h], b[4 * h + 1], b[4 * h + 2], b[4 * h + 3]);
       }
     }
+  }
+}
+
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(256, NV <= (V == 4 ? 24 : 16) ? 2 : 1) ln_forward_warp_kernel(const LnParams p) {
+  extern __shared__ __align__(16) float ln_smem[];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, cols = (int)p.cols, nvec = cols / V;
+  const int64_t group = blockIdx.x / p.splits, split = blockIdx.x - group * p.splits;
+  const bool affine = p.gain || p.bias;
+  if (affine) {
+    ln_stage_params<V>(p, group, ln_smem);
+    __syncthreads();
+  }
+  const float inv_c = 1.0f / (float)cols;
+  for (int64_t lr = split * 8 + (threadIdx.x >> 5); lr < p.group_rows; lr += p.splits * 8) {
+    const int64_t row = group * p.group_rows + lr;
+    const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx;
+    uint4 q[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = lane + i * 32;
+      q[i] = j < nvec ? load_vec<T, V>(x + j * V) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    // a vector is summed by itself first: short chains, small rounding errors
+    uint64_t s2 = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      uint64_t v[V / 2];
+      unpack_vec2<T, V>(q[i], v);
+      uint64_t t = v[0];
+#pragma unroll
+      for (int k = 1; k < V / 2; ++k) t = add_f32x2(t, v[k]);
+      s2 = add_f32x2(s2, t);
+    }
+    const float mean = warp_sum(sum_f32x2(s2)) * inv_c;
+    const uint64_t nm2 = pack_f32x2(-mean, -mean);
+    s2 = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (lane + i * 32 < nvec) {
+        uint64_t v[V / 2];
+        unpack_vec2<T, V>(q[i], v);
+        uint64_t t = 0;
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {
+          const uint64_t d = add_f32x2(v[k], nm2);
+          t = fma_f32x2(d, d, t);
+        }
+        s2 = add_f32x2(s2, t);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(warp_sum(sum_f32x2(s2)) * inv_c + p.eps);
+    if (lane == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    const uint64_t rs2 = pack_f32x2(rstd, rstd);
+    T* y = reinterpret_cast<T*>(p.out) + row * p.ldo;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = lane + i * 32;
+      if (j < nvec) {
+        uint64_t v[V / 2];
+        unpack_vec2<T, V>(q[i], v);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) v[k] = mul_f32x2(add_f32x2(v[k], nm2), rs2);
+        if (affine) {
+#pragma unroll
+          for (int h = 0; h < V / 4; ++h) {
+            const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(ln_smem + (h * nvec + j) * 4);
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(ln_smem + cols + (h * nvec + j) * 4);
+            v[2 * h] = fma_f32x2(v[2 * h], g.x, b.x);
+            v[2 * h + 1] = fma_f32x2(v[2 * h + 1], g.y, b.y);
+          }
+        }
+        store_vec2<T, V>(y + j * V, v);
+      }
+    }
+  }
+}
+
+// The same for rows that cannot be read as vectors: single elements, the
+// second and third reading of the row from the caches.
+template <typename T>
+__global__ void __launch_bounds__(256, 5) ln_forward_warp1_kernel(const LnParams p) {
+  extern __shared__ __align__(16) float ln_smem[];  // [gain + plus][bias]
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, cols = (int)p.cols;
+  const int64_t group = blockIdx.x / p.splits, split = blockIdx.x - group * p.splits;
+  ln_stage_params<1>(p, group, ln_smem);
+  __syncthreads();
+  const float* gp = ln_smem + lane;
+  const float inv_c = 1.0f / (float)cols;
+  // f(index, value, exists) for the lane's columns, eight loads at a time
+  auto each = [&](const T* x, auto f) {
+    int c = 0;
+#pragma unroll 4
+    for (; c + 256 <= cols; c += 256) {
+      T v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = x[c + k * 32];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f(c + k * 32, k, to_f32(v[k]), true);
+    }
+    if (c < cols) {
+      T v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = c + k * 32 + lane < cols ? x[c + k * 32] : from_f32<T>(0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f(c + k * 32, k, to_f32(v[k]), c + k * 32 + lane < cols);
+    }
   };
-  if (p.ptype == KL_BF16)
-    finish(std::integral_constant<int, KL_BF16>());
-  else if (p.ptype == KL_F16)
-    finish(std::integral_constant<int, KL_F16>());
-  else
-    finish(std::integral_constant<int, KL_F32>());
+  for (int64_t lr = split * 8 + (threadIdx.x >> 5); lr < p.group_rows; lr += p.splits * 8) {
+    const int64_t row = group * p.group_rows + lr;
+    const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx + lane;
+    T* y = reinterpret_cast<T*>(p.out) + row * p.ldo + lane;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    each(x, [&](int, int k, float v, bool) { s[k & 3] += v; });
+    const float mean = warp_sum((s[0] + s[1]) + (s[2] + s[3])) * inv_c;
+    s[0] = s[1] = s[2] = s[3] = 0.f;
+    each(x, [&](int, int k, float v, bool in) {
+      const float d = in ? v - mean : 0.f;
+      s[k & 3] = fmaf(d, d, s[k & 3]);
+    });
+    const float rstd = 1.0f / sqrtf(warp_sum((s[0] + s[1]) + (s[2] + s[3])) * inv_c + p.eps);
+    if (lane == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    each(x, [&](int c, int, float v, bool in) {
+      if (in) y[c] = from_f32<T>(fmaf((v - mean) * rstd, gp[c], gp[cols + c]));
+    });
+  }
 }
 
 // Rows wider than the register kernels hold: one CTA a row, re-reading it.
@@ -433,10 +524,16 @@ __global__ void __launch_bounds__(512, NV == 1 || V == 1 ? 2 : 1)
       for (int i = 0; i < NV; ++i) {
         const int64_t c = (int64_t)(threadIdx.x + i * blockDim.x) * V;
         if (c < p.cols) {
+          if constexpr (V == 1) {
+            out[c] = sg[i][0];
+            out[p.cols + c] = sb[i][0];
+          } else {
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            out[c + k] = sg[i][k];
-            out[p.cols + c + k] = sb[i][k];
+            for (int k = 0; k < V; k += 4) {
+              *reinterpret_cast<float4*>(out + c + k) = make_float4(sg[i][k], sg[i][k + 1], sg[i][k + 2], sg[i][k + 3]);
+              *reinterpret_cast<float4*>(out + p.cols + c + k) =
+                  make_float4(sb[i][k], sb[i][k + 1], sb[i][k + 2], sb[i][k + 3]);
+            }
           }
         }
       }
@@ -444,14 +541,15 @@ __global__ void __launch_bounds__(512, NV == 1 || V == 1 ? 2 : 1)
   }
 }
 
-// Many rows of at least 64 vectors: a CTA takes tiles of R rows of its group,
-// staged in shared memory by bulk copies a few tiles ahead (the row-at-a-time
-// kernel above has one row in flight and waits for it).  A thread owns NV
-// vectors of the columns in every row: it adds to the parameters' sums and to
-// the 2R row sums in one pass, the CTA joins the row sums once per tile, and a
-// second pass over the staged rows writes dx.
+// Many rows: a CTA takes tiles of R rows of its group; a thread owns E columns
+// in every row (their factors and sums stay in its registers), holds the tile's
+// values of its columns, adds them to the parameters' sums and to the 2R row
+// sums, which the CTA joins once per tile, and writes dx.  Arithmetic is on
+// packed pairs: unpacked it would bound the kernel instead of HBM.
+//
+// warp_sums: v[i] summed over the warp, into v[0] of the lanes with lane % N == i
 template <int N>
-__device__ __forceinline__ void warp_sums(float (&v)[N]) {  // v[i] summed over the warp into lanes with lane % N == i, all in v[0]
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int h = N / 2; h >= 1; h /= 2) {
@@ -466,32 +564,125 @@ __device__ __forceinline__ void warp_sums(float (&v)[N]) {  // v[i] summed over 
   for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
 }
 
-template <typename T, int NV, int R, bool PG>
-__global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 ? 2 : 1) ln_backward_tile_kernel(const LnParams p, int stages) {
-  constexpr int V = 16 / sizeof(T);
-  extern __shared__ __align__(16) uint8_t ln_tiles[];  // [stages][x, dy][R][cols]
-  __shared__ float red[2][NV == 1 ? 12 : 16][2 * R];
-  __shared__ uint64_t full[4];
+// Where rows are short a CTA, one a SM, is several teams of threads that take
+// tiles independently (a barrier each) and add their parameter sums through
+// shared memory at the end: one partial row a SM for the second kernel to read.
+constexpr int kLnTileRows = 2;
+constexpr int kLnTileWarps = 16;  // of a team, at most
+constexpr int kLnTeams = 12;      // at most (a team is at least two warps)
+__device__ __forceinline__ void team_sync(int team, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
+}
+
+// A team's sums of the columns at (c, c + step) join the others' and go out,
+// in the order of the teams.  buf: [teams][2][width]
+__device__ __forceinline__ void ln_join_teams(const float* buf, int teams, int width, int cols, float* out) {
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * width; c += blockDim.x) {
+    float s = buf[c];
+    for (int t = 1; t < teams; ++t) s += buf[t * 2 * width + c];
+    const int which = c >= width, col = c - which * width;
+    if (col < cols) out[(int64_t)which * cols + col] = s;
+  }
+}
+
+// what a thread keeps over the tiles, and one tile's arithmetic
+template <int E, bool PG>
+struct LnColumns {
+  static constexpr int R = kLnTileRows;
+  uint64_t g[E / 2], sg[PG ? E / 2 : 1], sb[PG ? E / 2 : 1];
+  __device__ __forceinline__ void clear() {
+    if constexpr (PG) {
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) sg[k] = sb[k] = 0;
+    }
+  }
+  // x, dy of the rows -> x - mean and dy; the thread's part of the row sums of
+  // h and h (x - mean).  Columns and rows that do not exist hold dy = 0.
+  __device__ __forceinline__ void sums(uint64_t (&x)[R][E / 2], const uint64_t (&d)[R][E / 2], const float (&m)[R],
+                                       const float (&rs)[R], float (&s)[2 * R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t nm2 = pack_f32x2(-m[r], -m[r]), rs2 = pack_f32x2(rs[r], rs[r]);
+      uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        x[r][k] = add_f32x2(x[r][k], nm2);
+        const uint64_t u = mul_f32x2(d[r][k], x[r][k]);  // dy * xhat / rstd
+        if constexpr (PG) {
+          sg[k] = fma_f32x2(u, rs2, sg[k]);
+          sb[k] = add_f32x2(sb[k], d[r][k]);
+        }
+        s0 = fma_f32x2(d[r][k], g[k], s0);
+        s1 = fma_f32x2(u, g[k], s1);
+      }
+      s[2 * r] = sum_f32x2(s0);
+      s[2 * r + 1] = sum_f32x2(s1);
+    }
+    warp_sums<2 * R>(s);
+  }
+  // the tile's row sums over the CTA from the warps' ([warps][2R]); warps past
+  // nw hold zeros.  tot[i]: i-th sum, in every lane
+  static __device__ __forceinline__ void join(const float* red, int nw, float (&tot)[2 * R]) {
+    static_assert(R == 2 && kLnTileWarps == 16, "two sums of 16 warps a register");
+    const int lane = threadIdx.x & 31, w = lane & 15, hi = lane >> 4;
+    float a = w < nw ? red[w * 4 + hi] : 0.f, b = w < nw ? red[w * 4 + 2 + hi] : 0.f;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    const float a2 = __shfl_xor_sync(0xffffffffu, a, 16), b2 = __shfl_xor_sync(0xffffffffu, b, 16);
+    tot[0] = hi ? a2 : a;
+    tot[1] = hi ? a : a2;
+    tot[2] = hi ? b2 : b;
+    tot[3] = hi ? b : b2;
+  }
+  // dx = rs * (h - mean(h) - (x - m) * rs * (rs * mean(h (x - m)))) of row r
+  __device__ __forceinline__ void dx(const uint64_t (&x)[E / 2], const uint64_t (&d)[E / 2], float rs, float mh,
+                                     float mhx, uint64_t (&o)[E / 2]) const {
+    const float a = -rs * (rs * mhx);
+    const uint64_t a2 = pack_f32x2(a, a), b2 = pack_f32x2(-mh, -mh), rs2 = pack_f32x2(rs, rs);
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) o[k] = mul_f32x2(rs2, fma_f32x2(d[k], g[k], fma_f32x2(x[k], a2, b2)));
+  }
+};
+
+// Rows of vectors: tiles are staged in shared memory by bulk copies a few
+// tiles ahead.
+template <typename T, int NV, bool PG, bool TEAMS>
+__global__ void __launch_bounds__(TEAMS ? 512 : 384, !TEAMS && NV * 16 / sizeof(T) <= 8 ? 2 : 1)
+    ln_backward_tile_kernel(const LnParams p, int team_threads, int stages) {
+  constexpr int V = 16 / sizeof(T), E = NV * V, R = kLnTileRows;
+  extern __shared__ __align__(16) uint8_t ln_tiles[];  // [team][stages][x, dy][R][cols]
+  __shared__ float red[TEAMS ? kLnTeams : 1][2][kLnTileWarps][2 * R];
+  __shared__ uint64_t full_all[TEAMS ? kLnTeams : 1][4];
   __shared__ int abort_smem;
   volatile int* abort_flag = &abort_smem;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5;
-  if (tid == 0) {
-    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+  const int tx = TEAMS ? team_threads : blockDim.x;
+  const int teams = TEAMS ? blockDim.x / tx : 1, team = TEAMS ? threadIdx.x / tx : 0;
+  const int tid = threadIdx.x - team * tx;
+  const int warp = tid >> 5, lane = tid & 31, nw = tx >> 5;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < teams; ++t)
+      for (int i = 0; i < stages; ++i) mbar_init(&full_all[t][i], 1);
     abort_smem = 0;
     fence_mbar_init();
   }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+  uint64_t* full = full_all[team];
   const int cols = (int)p.cols;
-  const int64_t group = blockIdx.x / p.splits, split = blockIdx.x - group * p.splits;
+  const int group = blockIdx.x / p.splits, split = (blockIdx.x - group * p.splits) * teams + team;
+  const int step = p.splits * teams, rows = (int)p.group_rows, tiles = (rows - 1) / R + 1;
   const int64_t r0 = group * p.group_rows;
-  const int64_t tiles = (p.group_rows + R - 1) / R;
   const uint32_t row_bytes = (uint32_t)cols * sizeof(T), half = row_bytes * R;
-  auto issue = [&](int64_t tile, int st) {  // thread 0
-    const int n = (int)min((int64_t)R, p.group_rows - tile * R);
+  uint8_t* mine = ln_tiles + (size_t)team * stages * 2 * half;
+  auto issue = [&](int tile, int st) {  // the team's thread 0
+    const int n = min(R, rows - tile * R);
     mbar_arrive_expect_tx(&full[st], 2 * n * row_bytes);
-    uint8_t* dst = ln_tiles + (size_t)st * 2 * half;
+    uint8_t* dst = mine + (size_t)st * 2 * half;
     for (int r = 0; r < n; ++r) {
       const int64_t row = r0 + tile * R + r;
       bulk_load(dst + r * row_bytes, reinterpret_cast<const T*>(p.x) + row * p.ldx, row_bytes, &full[st]);
@@ -500,102 +691,83 @@ __global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 ? 2 : 1) ln_backw
   };
   if (tid == 0)
     for (int i = 0; i < stages - 1; ++i)
-      if (split + (int64_t)i * p.splits < tiles) issue(split + (int64_t)i * p.splits, i);
-  // lane r holds row r's statistics of the next tile
-  float nmean = 0.f, nrstd = 0.f;
-  auto stats = [&](int64_t tile) {
-    const int64_t lr = tile * R + lane;
-    const bool in = lane < R && lr < p.group_rows;
-    nmean = in ? p.mean[r0 + lr] : 0.f;
-    nrstd = in ? p.rstd[r0 + lr] : 0.f;
+      if (split + i * step < tiles) issue(split + i * step, i);
+  // lane r holds the next tile's row r's statistics
+  float next_mean = 0.f, next_rstd = 0.f;
+  auto stats = [&](int tile) {
+    const int lr = tile * R + lane;
+    const bool in = lane < R && lr < rows;
+    next_mean = in ? __ldg(p.mean + r0 + lr) : 0.f;
+    next_rstd = in ? __ldg(p.rstd + r0 + lr) : 0.f;
   };
   stats(split);
   const float inv_c = 1.0f / (float)cols;
-  float g[NV][V], sg[PG ? NV : 1][V], sb[PG ? NV : 1][V];
+  LnColumns<E, PG> col;
+  col.clear();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (tid + i * (int)blockDim.x) * V;
-    ln_factor<V>(p, group * p.cols + c, c < cols, g[i]);
-  }
-  if constexpr (PG) {
+    const int c = (tid + i * tx) * V;
+    float g[V];
+    ln_factor<V>(p, (int64_t)group * cols + c, c < cols, g);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < V; ++k) sg[i][k] = sb[i][k] = 0.f;
+    for (int k = 0; k < V / 2; ++k) col.g[i * V / 2 + k] = pack_f32x2(g[2 * k], g[2 * k + 1]);
   }
-  int st = 0, buf = 0, issued = 0;
+  int st = 0, buf = 0, done = 0;
   uint32_t phase = 0;
-  for (int64_t tile = split; tile < tiles; tile += p.splits, buf ^= 1) {
-    const int n = (int)min((int64_t)R, p.group_rows - tile * R);
-    const float mean_l = nmean, rstd_l = nrstd;
-    if (tile + p.splits < tiles) stats(tile + p.splits);
+  for (int tile = split; tile < tiles; tile += step, buf ^= 1) {
+    const int n = min(R, rows - tile * R);
+    float m[R], rs[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = __shfl_sync(0xffffffffu, next_mean, r);
+      rs[r] = __shfl_sync(0xffffffffu, next_rstd, r);
+    }
+    if (tile + step < tiles) stats(tile + step);
     // a wait that runs out is recorded and the turns go on: every thread takes
     // the same barriers, and the results are then void
     warp_wait(&full[st], phase, abort_flag);
-    const T* xs = reinterpret_cast<const T*>(ln_tiles + (size_t)st * 2 * half);
-    const T* ds = reinterpret_cast<const T*>(ln_tiles + (size_t)st * 2 * half + half);
-    float s[2 * R];
+    const uint8_t* xs = mine + (size_t)st * 2 * half;
+    uint64_t x[R][E / 2], d[R][E / 2];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      s[2 * r] = s[2 * r + 1] = 0.f;
-      const float m = __shfl_sync(0xffffffffu, mean_l, r), rs = __shfl_sync(0xffffffffu, rstd_l, r);
-      if (r < n) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = (tid + i * (int)blockDim.x) * V;
-          if (c < cols) {
-            float xv[V], dv[V];
-            unpack_vec<T, V>(*reinterpret_cast<const uint4*>(xs + r * cols + c), xv);
-            unpack_vec<T, V>(*reinterpret_cast<const uint4*>(ds + r * cols + c), dv);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-              const float u = dv[k] * (xv[k] - m);  // dy * xhat / rstd
-              if constexpr (PG) {
-                sg[i][k] = fmaf(u, rs, sg[i][k]);
-                sb[i][k] += dv[k];
-              }
-              s[2 * r] = fmaf(dv[k], g[i][k], s[2 * r]);
-              s[2 * r + 1] = fmaf(u, g[i][k], s[2 * r + 1]);
-            }
-          }
-        }
+      for (int i = 0; i < NV; ++i) {
+        const int at = tid + i * tx;
+        const bool in = r < n && at * V < cols;
+        const uint4 qx = in ? *reinterpret_cast<const uint4*>(xs + r * row_bytes + at * 16) : make_uint4(0, 0, 0, 0);
+        const uint4 qd =
+            in ? *reinterpret_cast<const uint4*>(xs + half + r * row_bytes + at * 16) : make_uint4(0, 0, 0, 0);
+        unpack_vec2<T, V>(qx, *reinterpret_cast<uint64_t(*)[V / 2]>(&x[r][i * V / 2]));
+        unpack_vec2<T, V>(qd, *reinterpret_cast<uint64_t(*)[V / 2]>(&d[r][i * V / 2]));
       }
-    }
-    warp_sums<2 * R>(s);
-    if (lane < 2 * R) red[buf][warp][lane] = s[0];
-    __syncthreads();
-    // every thread is past the tile before this one: its stage is free
+    float s[2 * R], tot[2 * R];
+    col.sums(x, d, m, rs, s);
+    if (lane < 2 * R) red[team][buf][warp][lane] = s[0];
+    if constexpr (TEAMS)
+      team_sync(team, tx);
+    else
+      __syncthreads();
+    // every thread holds this tile in registers: the stage before it has been
+    // free for a turn, and is loaded again
     if (tid == 0) {
-      const int64_t next = tile + (int64_t)(stages - 1) * p.splits;
+      const int next = tile + (stages - 1) * step;
       if (next < tiles) issue(next, st == 0 ? stages - 1 : st - 1);
     }
-    float tot = 0.f;
-    if (lane < 2 * R)
-      for (int w = 0; w < nw; ++w) tot += red[buf][w][lane];
-    tot *= inv_c;
+    col.join(&red[team][buf][0][0], nw, tot);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float m = __shfl_sync(0xffffffffu, mean_l, r), rs = __shfl_sync(0xffffffffu, rstd_l, r);
-      // dx = rs * (h - mean(h) - (x - m) * rs * (rs * mean(h (x - m))))
-      const float b = -__shfl_sync(0xffffffffu, tot, 2 * r);
-      const float a = -rs * (rs * __shfl_sync(0xffffffffu, tot, 2 * r + 1));
       if (r < n) {
+        uint64_t o[E / 2];
+        col.dx(x[r], d[r], rs[r], tot[2 * r] * inv_c, tot[2 * r + 1] * inv_c, o);
         T* dx = reinterpret_cast<T*>(p.out) + (r0 + tile * R + r) * p.ldo;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = (tid + i * (int)blockDim.x) * V;
-          if (c < cols) {
-            float xv[V], dv[V];
-            unpack_vec<T, V>(*reinterpret_cast<const uint4*>(xs + r * cols + c), xv);
-            unpack_vec<T, V>(*reinterpret_cast<const uint4*>(ds + r * cols + c), dv);
-#pragma unroll
-            for (int k = 0; k < V; ++k) dv[k] = rs * fmaf(dv[k], g[i][k], fmaf(xv[k] - m, a, b));
-            store_vec<T, V>(dx + c, dv);
-          }
+          const int c = (tid + i * tx) * V;
+          if (c < cols) store_vec2<T, V>(dx + c, *reinterpret_cast<uint64_t(*)[V / 2]>(&o[i * V / 2]));
         }
       }
     }
-    ++issued;
+    ++done;
     if (++st == stages) {
       st = 0;
       phase ^= 1u;
@@ -604,22 +776,133 @@ __global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 ? 2 : 1) ln_backw
   if (tid == 0 && *abort_flag) {
     // the copies of the last tiles land before the CTA can leave
     volatile int no_abort = 0;
-    for (int i = max(0, issued - stages); i < issued; ++i)
+    for (int i = max(0, done - stages); i < done; ++i)
       mbar_wait(&full[i % stages], (uint32_t)((i / stages) & 1), &no_abort);
   }
   if constexpr (PG) {
+    // the stages become the teams' sums (nothing is on its way to them)
     float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
+    float* sums = TEAMS ? reinterpret_cast<float*>(ln_tiles) + team * 2 * cols : out;
+    if constexpr (TEAMS) __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (tid + i * (int)blockDim.x) * V;
+      const int c = (tid + i * tx) * V;
       if (c < cols) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          out[c + k] = sg[i][k];
-          out[p.cols + c + k] = sb[i][k];
+        for (int k = 0; k < V / 2; k += 2) {
+          *reinterpret_cast<ulonglong2*>(sums + c + 2 * k) = make_ulonglong2(col.sg[i * V / 2 + k], col.sg[i * V / 2 + k + 1]);
+          *reinterpret_cast<ulonglong2*>(sums + cols + c + 2 * k) =
+              make_ulonglong2(col.sb[i * V / 2 + k], col.sb[i * V / 2 + k + 1]);
         }
       }
     }
+    if constexpr (TEAMS) ln_join_teams(reinterpret_cast<const float*>(ln_tiles), teams, cols, cols, out);
+  }
+}
+
+// Rows that cannot be read as vectors: a thread owns every 32nd column of its
+// warp's 32 E, and loads the next tile's values before it works on this one's.
+template <typename T, int E, bool PG>
+__global__ void __launch_bounds__(E == 4 ? 768 : 512) ln_backward_tile1_kernel(const LnParams p, int tx) {
+  constexpr int R = kLnTileRows;
+  extern __shared__ float ln_sums[];  // [team][2][32 E * warps]
+  __shared__ float red[kLnTeams][2][kLnTileWarps][2 * R];
+  pdl_wait();
+  pdl_trigger();
+  const int teams = blockDim.x / tx, team = threadIdx.x / tx, tid = threadIdx.x - team * tx;
+  const int warp = tid >> 5, lane = tid & 31, nw = tx >> 5;
+  const int cols = (int)p.cols, c0 = warp * 32 * E + lane;
+  const bool full = (warp + 1) * 32 * E <= cols;  // every column of the warp exists
+  const int group = blockIdx.x / p.splits, split = (blockIdx.x - group * p.splits) * teams + team;
+  const int step = p.splits * teams, rows = (int)p.group_rows, tiles = (rows - 1) / R + 1;
+  const int64_t r0 = group * p.group_rows;
+  const float inv_c = 1.0f / (float)cols;
+  LnColumns<E, PG> col;
+  col.clear();
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) {
+    float ga[1], gb[1];
+    const int a = c0 + 64 * k, b = a + 32;
+    ln_factor<1>(p, (int64_t)group * cols + a, a < cols, ga);
+    ln_factor<1>(p, (int64_t)group * cols + b, b < cols, gb);
+    col.g[k] = pack_f32x2(ga[0], gb[0]);
+  }
+  T rx[R][E], rd[R][E];
+  float next_mean = 0.f, next_rstd = 0.f;  // lane r: row r's
+  auto fetch = [&](int tile) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool live = tile * R + r < rows;
+      const int64_t row = r0 + (live ? tile * R + r : 0);
+      const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx + c0;
+      const T* d = reinterpret_cast<const T*>(p.dy) + row * p.ldy + c0;
+      if (live && full) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          rx[r][k] = x[32 * k];
+          rd[r][k] = d[32 * k];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          const bool in = live && c0 + 32 * k < cols;
+          rx[r][k] = in ? x[32 * k] : from_f32<T>(0.f);
+          rd[r][k] = in ? d[32 * k] : from_f32<T>(0.f);
+        }
+      }
+    }
+    const int lr = tile * R + lane;
+    const bool in = lane < R && lr < rows;
+    next_mean = in ? __ldg(p.mean + r0 + lr) : 0.f;
+    next_rstd = in ? __ldg(p.rstd + r0 + lr) : 0.f;
+  };
+  if (split < tiles) fetch(split);
+  int buf = 0;
+  for (int tile = split; tile < tiles; tile += step, buf ^= 1) {
+    const int n = min(R, rows - tile * R);
+    float m[R], rs[R];
+    uint64_t x[R][E / 2], d[R][E / 2];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = __shfl_sync(0xffffffffu, next_mean, r);
+      rs[r] = __shfl_sync(0xffffffffu, next_rstd, r);
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        x[r][k] = pack_f32x2(to_f32(rx[r][2 * k]), to_f32(rx[r][2 * k + 1]));
+        d[r][k] = pack_f32x2(to_f32(rd[r][2 * k]), to_f32(rd[r][2 * k + 1]));
+      }
+    }
+    if (tile + step < tiles) fetch(tile + step);
+    float s[2 * R], tot[2 * R];
+    col.sums(x, d, m, rs, s);
+    if (lane < 2 * R) red[team][buf][warp][lane] = s[0];
+    team_sync(team, tx);
+    col.join(&red[team][buf][0][0], nw, tot);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r < n) {
+        uint64_t o[E / 2];
+        col.dx(x[r], d[r], rs[r], tot[2 * r] * inv_c, tot[2 * r + 1] * inv_c, o);
+        T* dx = reinterpret_cast<T*>(p.out) + (r0 + tile * R + r) * p.ldo + c0;
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+          float lo, hi;
+          unpack_f32x2(o[k], lo, hi);
+          if (full || c0 + 64 * k < cols) dx[64 * k] = from_f32<T>(lo);
+          if (full || c0 + 64 * k + 32 < cols) dx[64 * k + 32] = from_f32<T>(hi);
+        }
+      }
+    }
+  }
+  if constexpr (PG) {
+    const int width = nw * 32 * E;
+    float* sums = ln_sums + team * 2 * width + c0;
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+      unpack_f32x2(col.sg[k], sums[64 * k], sums[64 * k + 32]);
+      unpack_f32x2(col.sb[k], sums[width + 64 * k], sums[width + 64 * k + 32]);
+    }
+    ln_join_teams(ln_sums, teams, width, cols, p.part + (int64_t)blockIdx.x * 2 * p.cols);
   }
 }
 
@@ -703,8 +986,9 @@ __global__ void __launch_bounds__(512) ln_param_sum_kernel(const float* __restri
 }
 
 // ---------------------------------------------------------------- launchers
-// From this many rows on a warp takes a row; fewer rows leave SMs idle that
-// way, and a CTA takes one (short rows: always a warp).
+// From this many rows on a warp takes a row; fewer leave SMs idle that way,
+// and a CTA takes one (as for groups of a few rows, whose parameters would be
+// staged for nothing).
 constexpr int64_t kLnWarpRows = 4 * kNumSMs;
 
 // How a row is spread over threads: vectors of V elements where every row
@@ -741,30 +1025,51 @@ static int ln_splits(int64_t groups, int64_t group_rows, const LnShape& sh) {
   return (int)(s < most ? s : most);
 }
 
-// The backward's tile kernel: threads, CTAs of an SM and of a group, stages.
-// ok: rows of 64 to 1024 vectors, and tiles enough to give every SM two.
+// CTAs of a group of rows: `ctas` over all groups, at most one for `unit` rows
+static int64_t ln_ctas(int64_t groups, int64_t group_rows, int64_t ctas, int64_t unit) {
+  const int64_t s = ctas / groups, most = (group_rows + unit - 1) / unit;
+  return s < 1 ? 1 : s < most ? s : most;
+}
+
+// The backward's tile kernels.  bf16 rows of 193 to 384 vectors give a thread
+// two of them: 20,992 x 3,072 takes 65.6 us so and 72.8 with one, the work of
+// joining the row sums being the same for a thread of 8 columns and one of 16.
+// LnTile: threads of a team, teams, columns a thread,
+// stages (0: single elements), CTAs of a group.  ok: 64 to 768 (fp32: 1152)
+// vectors a row, or 256 to 4096 single elements, and rows enough for half the SMs.
 struct LnTile {
   bool ok;
-  int nv, tx, rows, stages, splits;
+  int n, tx, teams, stages, splits;  // n: vectors, or single columns, of a thread
 };
 static LnTile ln_tile(int64_t groups, int64_t group_rows, int64_t cols, int es, bool vec) {
   LnTile t{};
-  if (!vec) return t;
-  const int64_t n = cols / (16 / es);
-  if (n < 64 || n > 1024) return t;
-  t.nv = n <= 384 ? 1 : 2;
-  t.tx = (int)(((n + t.nv - 1) / t.nv + 31) / 32 * 32);
-  const int per_sm = (t.nv == 1 ? 768 : 512) / t.tx;
-  const int64_t row = 2 * cols * es, budget = (int64_t)216 * 1024 / per_sm;
-  t.rows = budget / (4 * row) >= 3 ? 4 : 2;
-  const int64_t st = budget / (t.rows * row);
-  t.stages = (int)(st > 4 ? 4 : st);
-  const int64_t tiles = (group_rows + t.rows - 1) / t.rows;
-  int64_t s = (int64_t)kNumSMs * per_sm / groups;
-  s = s < tiles / 2 ? s : tiles / 2;
-  s = s < 1 ? 1 : s;
+  int threads, per_sm = 1;
+  if (vec) {
+    const int64_t n = cols / (16 / es);
+    if (n < 64 || n > (es == 4 ? 1152 : 768)) return t;
+    t.n = es == 2 && n > 192 && n <= 384 ? 2 : (int)((n + 383) / 384);
+    t.tx = (int)(((n + t.n - 1) / t.n + 31) / 32 * 32);
+    threads = t.tx <= 192 && t.n == 1 ? 512 : t.tx;
+    per_sm = (t.tx > 192 && t.n * 16 / es <= 8) || (t.n == 2 && t.tx <= 192) ? 2 : 1;
+  } else {
+    if (cols < 256 || cols > 4096) return t;
+    t.n = cols <= 1024 ? 4 : 8;
+    t.tx = (int)((cols + 32 * t.n - 1) / (32 * t.n) * 32);
+    threads = t.n == 4 ? 768 : 512;
+  }
+  const int64_t s = ln_ctas(groups, group_rows, kNumSMs * per_sm, 2 * kLnTileRows);
   t.splits = (int)s;
-  t.ok = t.stages >= 2 && tiles >= 2 && s * groups >= kNumSMs;
+  // no team without two tiles
+  int64_t teams = group_rows / (2 * kLnTileRows * s);
+  teams = teams < 1 ? 1 : teams;
+  t.teams = threads / t.tx;
+  if (t.teams > teams) t.teams = (int)teams;
+  if (vec) {
+    const int64_t stage = 2 * kLnTileRows * cols * es, budget = (int64_t)216 * 1024 / (t.teams * per_sm);
+    t.stages = (int)(budget / stage > 4 ? 4 : budget / stage);
+    if (t.stages < 2) return t;
+  }
+  t.ok = group_rows >= 2 * kLnTileRows && s * groups >= kNumSMs / 2;
   return t;
 }
 
@@ -774,28 +1079,39 @@ static cudaError_t launch_ln_forward_nv(const LnParams& p, const LnShape& sh, cu
                     (size_t)sh.ty * 64 * sizeof(float), s, p);
 }
 template <typename T, int V, int NV>
-static cudaError_t launch_ln_forward_warp(const LnParams& p, cudaStream_t s) {
-  return launch_pdl(ln_forward_warp_kernel<T, V, NV>, dim3((unsigned)((p.rows + 3) / 4)), dim3(128), 0, s, p);
+static cudaError_t launch_ln_forward_warp(LnParams& p, cudaStream_t s) {
+  const size_t smem = p.gain || p.bias ? (size_t)p.cols * 8 : 0;
+  const int per_sm = NV * V <= 16 ? 5 : NV * V <= 32 ? 3 : NV <= (V == 4 ? 24 : 16) ? 2 : 1;
+  const int64_t groups = p.rows / p.group_rows;
+  p.splits = (int)ln_ctas(groups, p.group_rows, (int64_t)kNumSMs * per_sm, 8);
+  const cudaError_t e = cudaFuncSetAttribute(ln_forward_warp_kernel<T, V, NV>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * NV * V * 8);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(ln_forward_warp_kernel<T, V, NV>, dim3((unsigned)(groups * p.splits)), dim3(256), smem, s, p);
 }
 template <typename T>
-static cudaError_t launch_ln_forward(const LnParams& p, bool vec, cudaStream_t s) {
+static cudaError_t launch_ln_forward(LnParams& p, bool vec, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const int64_t lanes = (p.cols + 31) / 32;
-  if (p.rows >= kLnWarpRows || lanes <= 4 * V) {
+  if (p.rows >= kLnWarpRows && p.group_rows >= 16) {
+    const int64_t groups = p.rows / p.group_rows, nv = (p.cols / V + 31) / 32;
     if (vec) {
-      const int64_t nv = (p.cols / V + 31) / 32;
       if (nv <= 1) return launch_ln_forward_warp<T, V, 1>(p, s);
       if (nv <= 2) return launch_ln_forward_warp<T, V, 2>(p, s);
       if (nv <= 4) return launch_ln_forward_warp<T, V, 4>(p, s);
       if (nv <= 8) return launch_ln_forward_warp<T, V, 8>(p, s);
       if (nv <= 12) return launch_ln_forward_warp<T, V, 12>(p, s);
       if (nv <= 16) return launch_ln_forward_warp<T, V, 16>(p, s);
-    } else {
-      if (lanes <= 4) return launch_ln_forward_warp<T, 1, 4>(p, s);
-      if (lanes <= 16) return launch_ln_forward_warp<T, 1, 16>(p, s);
-      if (lanes <= 32) return launch_ln_forward_warp<T, 1, 32>(p, s);
-      if (lanes <= 48) return launch_ln_forward_warp<T, 1, 48>(p, s);
-      if (lanes <= 64) return launch_ln_forward_warp<T, 1, 64>(p, s);
+      if (nv <= 24) return launch_ln_forward_warp<T, V, 24>(p, s);
+      if constexpr (V == 4) {
+        if (nv <= 32) return launch_ln_forward_warp<T, 4, 32>(p, s);
+      }
+    } else if (p.cols <= 6144) {
+      const size_t smem = (size_t)p.cols * 8;
+      p.splits = (int)ln_ctas(groups, p.group_rows, kNumSMs * 5, 8);
+      const cudaError_t e =
+          cudaFuncSetAttribute(ln_forward_warp1_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 6144 * 8);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(ln_forward_warp1_kernel<T>, dim3((unsigned)(groups * p.splits)), dim3(256), smem, s, p);
     }
   }
   const LnShape sh = ln_shape(p.cols, sizeof(T), vec, false);
@@ -816,27 +1132,35 @@ static cudaError_t launch_ln_backward_nv(const LnParams& p, const LnShape& sh, c
   return p.part ? launch_pdl(ln_backward_kernel<T, V, NV, true>, grid, block, smem, s, p)
                 : launch_pdl(ln_backward_kernel<T, V, NV, false>, grid, block, smem, s, p);
 }
-template <typename T, int NV, int R, bool PG>
+template <typename T, int NV, bool PG, bool TEAMS>
 static cudaError_t launch_ln_tile(const LnParams& p, const LnTile& t, cudaStream_t s) {
-  const size_t smem = (size_t)t.stages * 2 * R * p.cols * sizeof(T);
-  const cudaError_t e = cudaFuncSetAttribute(ln_backward_tile_kernel<T, NV, R, PG>,
+  const size_t smem = (size_t)t.teams * t.stages * 2 * kLnTileRows * p.cols * sizeof(T);
+  const cudaError_t e = cudaFuncSetAttribute(ln_backward_tile_kernel<T, NV, PG, TEAMS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(ln_backward_tile_kernel<T, NV, R, PG>, dim3((unsigned)(p.rows / p.group_rows * p.splits)),
-                    dim3(t.tx), smem, s, p, t.stages);
+  return launch_pdl(ln_backward_tile_kernel<T, NV, PG, TEAMS>, dim3((unsigned)(p.rows / p.group_rows * p.splits)),
+                    dim3(t.tx * t.teams), smem, s, p, t.tx, t.stages);
 }
-template <typename T, int NV>
-static cudaError_t launch_ln_tile_nv(const LnParams& p, const LnTile& t, cudaStream_t s) {
-  if (t.rows == 4)
-    return p.part ? launch_ln_tile<T, NV, 4, true>(p, t, s) : launch_ln_tile<T, NV, 4, false>(p, t, s);
-  return p.part ? launch_ln_tile<T, NV, 2, true>(p, t, s) : launch_ln_tile<T, NV, 2, false>(p, t, s);
+template <typename T, bool PG>
+static cudaError_t launch_ln_tiles(const LnParams& p, const LnTile& t, bool vec, cudaStream_t s) {
+  if (!vec) {
+    const dim3 grid((unsigned)(p.rows / p.group_rows * p.splits)), block(t.tx * t.teams);
+    const size_t smem = PG ? (size_t)t.teams * t.tx * 2 * t.n * sizeof(float) : 0;  // at most 32 KB
+    return t.n == 4 ? launch_pdl(ln_backward_tile1_kernel<T, 4, PG>, grid, block, smem, s, p, t.tx)
+                    : launch_pdl(ln_backward_tile1_kernel<T, 8, PG>, grid, block, smem, s, p, t.tx);
+  }
+  if (t.n == 1) return t.tx <= 192 ? launch_ln_tile<T, 1, PG, true>(p, t, s) : launch_ln_tile<T, 1, PG, false>(p, t, s);
+  if constexpr (sizeof(T) == 4) {
+    if (t.n == 3) return launch_ln_tile<T, 3, PG, false>(p, t, s);
+  }
+  return launch_ln_tile<T, 2, PG, false>(p, t, s);
 }
 
 template <typename T>
 static cudaError_t launch_ln_backward(LnParams& p, bool vec, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const LnTile t = ln_tile(p.rows / p.group_rows, p.group_rows, p.cols, sizeof(T), vec);
-  if (t.ok) return t.nv == 1 ? launch_ln_tile_nv<T, 1>(p, t, s) : launch_ln_tile_nv<T, 2>(p, t, s);
+  if (t.ok) return p.part ? launch_ln_tiles<T, true>(p, t, vec, s) : launch_ln_tiles<T, false>(p, t, vec, s);
   const LnShape sh = ln_shape(p.cols, sizeof(T), vec, true);
   if (sh.nv == 0) {
     cudaError_t e = launch_pdl(ln_backward_wide_kernel<T>, dim3((unsigned)p.rows), dim3(1024), 256, s, p);

@@ -11,9 +11,10 @@
 // Angles: f_j / pi is made on the host in extended precision; position times
 // it is one fp64 product, reduced by whole turns exactly (h - 2 rint(h / 2)),
 // so positions far along an axis lose nothing; sincospif of the reduced angle
-// is fp32.  Each angle is used by every head of its token, so a CTA makes its
-// tokens' table in shared memory once and a thread keeps its pairs' cosines
-// and sines in registers over the heads.
+// is fp32.  Each angle is used by every head of its token: a CTA makes the
+// table of a few tokens in shared memory, then its threads walk the (token,
+// head) rows with four rows' loads in flight.  CTAs stay for many chunks of
+// tokens; two table buffers leave one barrier a chunk.
 //
 // Bound by HBM: one read and one write of the tensor; the fp64 work is one
 // angle per (token, pair), a head's share of it 1 / H.
@@ -27,18 +28,22 @@ namespace kl {
 
 constexpr int kRopeMaxPairs = 256;  // head dim 512
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;  // heads a thread loads before it stores the first
+constexpr int kRopeBatch = 4;       // rows a thread loads before it stores the first
+constexpr int kRopeTable = 2560;    // (token, pair) entries of a table buffer: two are 40 KB
 
 struct RopeParams {
   const void* x;
   void* out;
   const void* pos;
-  int64_t batch, tokens, heads;
+  int64_t batch, tokens;
   int64_t xs_b, xs_t, xs_h, os_b, os_t, os_h;  // strides in elements; dims are consecutive
   int64_t pos_b;                               // position rows between batches (0: shared)
+  int64_t chunks;                              // token chunks of a batch
+  int64_t items;                               // batch * chunks * head parts
+  int heads, hparts, hper;                     // a chunk's heads are in hparts parts of hper
   int dim, pairs, naxes, pos_type;
   int units;            // per head: vectors of dims (interleaved) or of pairs, then of copied dims (half)
-  int tok_per_cta;
+  int nt;               // tokens of a chunk
   float sign;           // -1: inverse
   int first[KL_ROPE_MAX_AXES + 1];  // first pair of each axis
   double freq[kRopeMaxPairs];       // f_j / pi
@@ -50,123 +55,137 @@ __device__ __forceinline__ double rope_pos(const RopeParams& p, int64_t i) {
   return (double)reinterpret_cast<const float*>(p.pos)[i];
 }
 
-// V elements a thread at a time (16 bytes, or V = 1 for what is not aligned;
-// interleaved pairs then move two elements).  A thread keeps one unit u of the
-// head and walks the heads: threads = units x slots.
+// one unit of one row: loaded, turned by the row's table entries, stored
 template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(512) rope_axes_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float2 rope_table_smem[];  // [tok_per_cta][pairs] (cos, sin)
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, nthreads = blockDim.x;
-  const int64_t chunks = (p.tokens + p.tok_per_cta - 1) / p.tok_per_cta;
-  const int64_t b = blockIdx.x / chunks, t0 = (blockIdx.x - b * chunks) * p.tok_per_cta;
-  const int nt = (int)min((int64_t)p.tok_per_cta, p.tokens - t0);
-  for (int i = tid; i < nt * p.pairs; i += nthreads) {
-    const int t = i / p.pairs, j = i - t * p.pairs;
-    int a = 0;
-    while (j >= p.first[a + 1]) ++a;
-    const double h = rope_pos(p, (b * p.pos_b + t0 + t) * p.naxes + a) * p.freq[j];
-    float s, c;
-    sincospif((float)(h - 2.0 * rint(0.5 * h)), &s, &c);
-    rope_table_smem[i] = make_float2(c, p.sign * s);
-  }
-  __syncthreads();
-  const int slots = nthreads / p.units;
-  const int u = tid % p.units, slot = tid / p.units;
-  if (slot >= slots) return;
-  constexpr int NP = HALF ? V : (V == 1 ? 1 : V / 2);  // pairs of a unit
-  const int pair_units = p.pairs / NP;
-  // first pair of the unit; interleaved units may reach past the last pair
-  const int j0 = u * NP;
-  const int64_t hstep = (int64_t)gridDim.y * slots;
-  for (int t = 0; t < nt; ++t) {
-    const T* xt = reinterpret_cast<const T*>(p.x) + b * p.xs_b + (t0 + t) * p.xs_t;
-    T* ot = reinterpret_cast<T*>(p.out) + b * p.os_b + (t0 + t) * p.os_t;
-    float2 cs[NP];
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
-      cs[i] = j0 + i < p.pairs ? rope_table_smem[t * p.pairs + j0 + i] : make_float2(1.f, 0.f);
-    const int64_t h0 = (int64_t)blockIdx.y * slots + slot;
+struct RopeUnit {
+  static constexpr int NP = HALF ? V : (V == 1 ? 1 : V / 2);  // pairs
+  uint4 a, c;  // c: the second halves, or the second element
+  __device__ __forceinline__ void load(const T* x, const RopeParams& p, int u, int pair_units) {
     if constexpr (HALF) {
       if (u < pair_units) {
-        // (loads of several heads ahead of the first store: x and out may be
-        // the same tensor, so the compiler cannot move them itself)
-        for (int64_t h = h0; h < p.heads; h += kRopeBatch * hstep) {
-          uint4 qa[kRopeBatch], qc[kRopeBatch];
-#pragma unroll
-          for (int k = 0; k < kRopeBatch; ++k) {
-            if (h + k * hstep < p.heads) {
-              const T* x = xt + (h + k * hstep) * p.xs_h + j0;
-              qa[k] = load_vec<T, V>(x);
-              qc[k] = load_vec<T, V>(x + p.pairs);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < kRopeBatch; ++k) {
-            if (h + k * hstep < p.heads) {
-              T* o = ot + (h + k * hstep) * p.os_h + j0;
-              float a[V], c[V];
-              unpack_vec<T, V>(qa[k], a);
-              unpack_vec<T, V>(qc[k], c);
-#pragma unroll
-              for (int i = 0; i < V; ++i) {
-                const float a0 = a[i], c0 = c[i];
-                a[i] = a0 * cs[i].x - c0 * cs[i].y;
-                c[i] = a0 * cs[i].y + c0 * cs[i].x;
-              }
-              store_vec<T, V>(o, a);
-              store_vec<T, V>(o + p.pairs, c);
-            }
-          }
-        }
+        a = load_vec<T, V>(x + u * V);
+        c = load_vec<T, V>(x + p.pairs + u * V);
       } else {
-        const int d = 2 * p.pairs + (u - pair_units) * V;
-        for (int64_t h = h0; h < p.heads; h += hstep) {
-          if constexpr (V == 1)
-            ot[h * p.os_h + d] = xt[h * p.xs_h + d];
-          else
-            *reinterpret_cast<uint4*>(ot + h * p.os_h + d) = load_vec<T, V>(xt + h * p.xs_h + d);
-        }
+        a = load_vec<T, V>(x + 2 * p.pairs + (u - pair_units) * V);
       }
     } else if constexpr (V == 1) {
-      const int d = 2 * u;
-      const bool turn = u < p.pairs, two = d + 1 < p.dim;
-      for (int64_t h = h0; h < p.heads; h += hstep) {
-        const T* x = xt + h * p.xs_h + d;
-        T* o = ot + h * p.os_h + d;
-        if (turn) {
-          const float a0 = to_f32(x[0]), c0 = to_f32(x[1]);
-          o[0] = from_f32<T>(a0 * cs[0].x - c0 * cs[0].y);
-          o[1] = from_f32<T>(a0 * cs[0].y + c0 * cs[0].x);
-        } else {
-          const T a0 = x[0];
-          if (two) o[1] = x[1];
-          o[0] = a0;
+      a = load_vec<T, 1>(x + 2 * u);
+      if (2 * u + 1 < p.dim) c = load_vec<T, 1>(x + 2 * u + 1);
+    } else {
+      a = load_vec<T, V>(x + u * V);
+    }
+  }
+  __device__ __forceinline__ void store(T* o, const RopeParams& p, int u, int pair_units, const float2* row) {
+    if constexpr (HALF || V == 1) {
+      float va[V], vc[V];
+      unpack_vec<T, V>(a, va);
+      if (u < pair_units) {
+        unpack_vec<T, V>(c, vc);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float2 cs = row[u * V + i];
+          const float x0 = va[i], x1 = vc[i];
+          va[i] = x0 * cs.x - x1 * cs.y;
+          vc[i] = x0 * cs.y + x1 * cs.x;
         }
+        if constexpr (HALF) {
+          store_vec<T, V>(o + u * V, va);
+          store_vec<T, V>(o + p.pairs + u * V, vc);
+        } else {
+          o[2 * u] = from_f32<T>(va[0]);
+          o[2 * u + 1] = from_f32<T>(vc[0]);
+        }
+      } else if constexpr (HALF) {
+        put(o + 2 * p.pairs + (u - pair_units) * V, a);
+      } else {
+        put(o + 2 * u, a);
+        if (2 * u + 1 < p.dim) put(o + 2 * u + 1, c);
       }
     } else {
-      for (int64_t h = h0; h < p.heads; h += kRopeBatch * hstep) {
-        uint4 q[kRopeBatch];
+      float v[V];
+      unpack_vec<T, V>(a, v);
 #pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k)
-          if (h + k * hstep < p.heads) q[k] = load_vec<T, V>(xt + (h + k * hstep) * p.xs_h + u * V);
+      for (int i = 0; i < NP; ++i) {
+        if (u * NP + i < p.pairs) {  // dims past the pairs stay as they are
+          const float2 cs = row[u * NP + i];
+          const float x0 = v[2 * i], x1 = v[2 * i + 1];
+          v[2 * i] = x0 * cs.x - x1 * cs.y;
+          v[2 * i + 1] = x0 * cs.y + x1 * cs.x;
+        }
+      }
+      store_vec<T, V>(o + u * V, v);
+    }
+  }
+  // the loaded bits themselves
+  static __device__ __forceinline__ void put(T* o, const uint4& q) {
+    if constexpr (V > 1)
+      *reinterpret_cast<uint4*>(o) = q;
+    else if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<uint32_t*>(o) = q.x;
+    else
+      *reinterpret_cast<uint16_t*>(o) = (uint16_t)q.x;
+  }
+};
+
+// V elements a thread at a time (16 bytes, or V = 1 for what is not aligned;
+// interleaved pairs then move two elements).  A thread keeps one unit u of the
+// head and walks the rows.
+template <typename T, int V, bool HALF>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_axes_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) float2 rope_tables[];  // [2][nt][pairs] (cos, sin)
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  // this thread's pair of the table, its frequency and axis
+  const int tslots = kRopeThreads / p.pairs, tj = tid % p.pairs, ts = tid / p.pairs;
+  const double freq = p.freq[tj];
+  int axis = 0;
+  while (tj >= p.first[axis + 1]) ++axis;
+  const int ulim = min(p.units, kRopeThreads), slots = kRopeThreads / ulim;
+  const int u0 = tid % ulim, slot = tid / ulim;
+  const int pair_units = HALF || V == 1 ? p.pairs / V : 0;
+  int buf = 0;
+  for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x, buf ^= 1) {
+    const int64_t bc = item / p.hparts, b = bc / p.chunks, t0 = (bc - b * p.chunks) * p.nt;
+    const int h0 = (int)(item - bc * p.hparts) * p.hper, nh = min(p.hper, p.heads - h0);
+    const int nt = (int)min((int64_t)p.nt, p.tokens - t0);
+    float2* table = rope_tables + buf * p.nt * p.pairs;
+    if (ts < tslots) {
+      for (int t = ts; t < nt; t += tslots) {
+        const double h = rope_pos(p, (b * p.pos_b + t0 + t) * p.naxes + axis) * freq;
+        float sn, cs;
+        sincospif((float)(h - 2.0 * rint(0.5 * h)), &sn, &cs);
+        table[t * p.pairs + tj] = make_float2(cs, p.sign * sn);
+      }
+    }
+    __syncthreads();
+    if (slot >= slots) continue;
+    const T* x = reinterpret_cast<const T*>(p.x) + b * p.xs_b + t0 * p.xs_t + h0 * p.xs_h;
+    T* o = reinterpret_cast<T*>(p.out) + b * p.os_b + t0 * p.os_t + h0 * p.os_h;
+    const int rows = nt * nh, dt = slots / nh, dh = slots - dt * nh;  // a step of `slots` rows
+    for (int u = u0; u < p.units; u += kRopeThreads) {
+      int t = slot / nh, h = slot - t * nh;
+      for (int r = slot; r < rows; r += kRopeBatch * slots) {
+        // several rows' loads ahead of the first store: x and out may be the
+        // same tensor, so the compiler cannot move them itself
+        RopeUnit<T, V, HALF> q[kRopeBatch];
+        int tt[kRopeBatch], hh[kRopeBatch];
 #pragma unroll
         for (int k = 0; k < kRopeBatch; ++k) {
-          if (h + k * hstep < p.heads) {
-            float v[V];
-            unpack_vec<T, V>(q[k], v);
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-              if (j0 + i < p.pairs) {  // dims past the pairs stay as they are
-                const float a0 = v[2 * i], c0 = v[2 * i + 1];
-                v[2 * i] = a0 * cs[i].x - c0 * cs[i].y;
-                v[2 * i + 1] = a0 * cs[i].y + c0 * cs[i].x;
-              }
-            }
-            store_vec<T, V>(ot + (h + k * hstep) * p.os_h + u * V, v);
+          tt[k] = t;
+          hh[k] = h;
+          if (r + k * slots < rows) q[k].load(x + t * p.xs_t + h * p.xs_h, p, u, pair_units);
+          t += dt;
+          h += dh;
+          if (h >= nh) {
+            h -= nh;
+            ++t;
           }
         }
+#pragma unroll
+        for (int k = 0; k < kRopeBatch; ++k)
+          if (r + k * slots < rows)
+            q[k].store(o + tt[k] * p.os_t + hh[k] * p.os_h, p, u, pair_units, table + tt[k] * p.pairs);
       }
     }
   }
@@ -175,23 +194,29 @@ __global__ void __launch_bounds__(512) rope_axes_kernel(const __grid_constant__ 
 template <typename T, int V>
 static cudaError_t launch_rope_v(RopeParams& p, bool half, cudaStream_t s) {
   p.units = half ? p.pairs / V + (p.dim - 2 * p.pairs) / V : (V == 1 ? (p.dim + 1) / 2 : p.dim / V);
-  const int slots = p.units >= kRopeThreads ? 1 : kRopeThreads / p.units;
-  const int threads = (p.units * slots + 31) / 32 * 32;
-  // a CTA takes several tokens once there are enough of them to fill the GPU
-  // (the table is then made once, by all threads); with few tokens the heads
-  // are split over CTAs instead
-  const int64_t total = p.batch * p.tokens, want = (int64_t)device_sm_count() * 8;
-  int tpc = (int)(total / want);
-  tpc = tpc < 1 ? 1 : tpc > 8 ? 8 : tpc;
-  p.tok_per_cta = tpc;
-  const int64_t gx = p.batch * ((p.tokens + tpc - 1) / tpc);
-  int64_t gy = total >= want ? 1 : (want + total - 1) / total;
-  const int64_t hchunks = (p.heads + slots - 1) / slots;
-  if (gy > hchunks) gy = hchunks;
-  if (gx > 0x7FFFFFFF || gy > 65535) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)tpc * p.pairs * sizeof(float2);
-  return half ? launch_pdl(rope_axes_kernel<T, V, true>, dim3((unsigned)gx, (unsigned)gy), dim3(threads), smem, s, p)
-              : launch_pdl(rope_axes_kernel<T, V, false>, dim3((unsigned)gx, (unsigned)gy), dim3(threads), smem, s, p);
+  // chunks of about 24 KB of x, within the table; smaller ones, then parts of
+  // the heads, where that leaves fewer than four a SM
+  const int64_t want = (int64_t)device_sm_count() * 4, total = p.batch * p.tokens;
+  const int64_t token_bytes = (int64_t)p.heads * p.dim * sizeof(T);
+  int64_t nt = 24576 / token_bytes, most = kRopeTable / p.pairs;
+  if (nt > total / want) nt = total / want;
+  if (nt > most) nt = most;
+  if (nt > p.tokens) nt = p.tokens;
+  if (nt < 1) nt = 1;
+  p.nt = (int)nt;
+  p.chunks = (p.tokens + nt - 1) / nt;
+  const int ulim = p.units < kRopeThreads ? p.units : kRopeThreads, slots = kRopeThreads / ulim;
+  int64_t parts = want / (p.batch * p.chunks);
+  const int64_t hchunks = (p.heads + slots - 1) / slots;  // no part without a row for every slot
+  if (parts > hchunks) parts = hchunks;
+  if (parts < 1) parts = 1;
+  p.hper = (int)((p.heads + parts - 1) / parts);
+  p.hparts = (p.heads + p.hper - 1) / p.hper;
+  p.items = p.batch * p.chunks * p.hparts;
+  const unsigned grid = (unsigned)(p.items < want ? p.items : want);
+  const size_t smem = (size_t)2 * nt * p.pairs * sizeof(float2);
+  return half ? launch_pdl(rope_axes_kernel<T, V, true>, dim3(grid), dim3(kRopeThreads), smem, s, p)
+              : launch_pdl(rope_axes_kernel<T, V, false>, dim3(grid), dim3(kRopeThreads), smem, s, p);
 }
 
 template <typename T>
@@ -226,7 +251,7 @@ extern "C" kl_status kl_rope_axes(const kl_rope_args* r, void* stream) {
       2 * pairs > r->dim)
     return KL_ERR_UNSUPPORTED_SHAPE;
   const int64_t lim = (int64_t)1 << 31;
-  if (r->batch >= lim || r->tokens >= lim || r->heads >= lim || r->batch > lim / r->tokens)
+  if (r->batch >= lim || r->tokens >= lim || r->heads >= lim / 2 || r->batch > lim / r->tokens)
     return KL_ERR_UNSUPPORTED_SHAPE;
   const int es = r->dtype == KL_F32 ? 4 : 2;
   if (!aligned(r->x, es) || !aligned(r->out, es) || !aligned(r->pos, r->pos_type == KL_POS_I64 ? 8 : 4))
@@ -238,7 +263,7 @@ extern "C" kl_status kl_rope_axes(const kl_rope_args* r, void* stream) {
   p.pos = r->pos;
   p.batch = r->batch;
   p.tokens = r->tokens;
-  p.heads = r->heads;
+  p.heads = (int)r->heads;
   p.xs_b = r->x_stride[0];
   p.xs_t = r->x_stride[1];
   p.xs_h = r->x_stride[2];
