@@ -14,9 +14,10 @@
 // a lane holds 16 columns, eight lanes a block, a warp four blocks -- the
 // four scale bytes of one 32-bit word of the MMA scale layout -- so the amax
 // is three shuffles and nothing goes through shared memory.  Tiles and
-// transposes stage a 128 x 128 tile in shared memory (transposes read it by
-// column pairs, 32 rows a thread, so a thread writes 32 contiguous bytes of
-// x^T).
+// transposes hold 128 rows of x in registers too: a thread of a transpose
+// reads column pairs of 16 rows and writes 16 contiguous bytes of x^T.
+#include <type_traits>
+
 #include "../../include/klein.h"
 #include "kl_common.cuh"
 #include "kl_internal.h"
@@ -37,12 +38,28 @@ __device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t amax_bits) {
 // 2^(127 - byte); byte <= 247 for finite blocks, so the result is normal
 __device__ __forceinline__ float fp8_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// four values -> four E4M3 bytes of a block (every code NaN if its byte is 255)
-__device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d, uint32_t byte) {
-  if (byte == 255u) return 0x7F7F7F7Fu;
-  const float inv = fp8_inv_scale(byte);
-  return f32x2_to_e4m3x2(__fmul_rn(a, inv), __fmul_rn(b, inv)) |
-         (f32x2_to_e4m3x2(__fmul_rn(c, inv), __fmul_rn(d, inv)) << 16);
+// what a block's values are multiplied by: 2^(127 - byte), or NaN
+__device__ __forceinline__ uint64_t fp8_inv2(uint32_t byte) {
+  const float inv = byte == 255u ? __uint_as_float(0x7FC00000u) : fp8_inv_scale(byte);
+  return pack_f32x2(inv, inv);
+}
+// four values -> four E4M3 bytes
+__device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d, uint64_t inv2) {
+  unpack_f32x2(mul_f32x2(pack_f32x2(a, b), inv2), a, b);
+  unpack_f32x2(mul_f32x2(pack_f32x2(c, d), inv2), c, d);
+  return f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(c, d) << 16);
+}
+// 16 codes, of which n >= 16 or the first n exist (the others are 0)
+__device__ __forceinline__ uint4 fp8_codes16(const float (&v)[16], uint64_t inv2, int n) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = fp8_codes4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], inv2);
+  if (n < 16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n < 4 * j + 4) w[j] = n <= 4 * j ? 0u : w[j] & ((1u << (8 * (n - 4 * j))) - 1u);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // byte offset of (row, block) in the MMA scale layout
@@ -50,30 +67,84 @@ __device__ __forceinline__ int64_t fp8_mma_offset(int64_t row, int64_t blk, int6
   return ((row >> 7) * atoms_k + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
 }
 
-// 16 consecutive elements of a row, of which `n` exist, as fp32
-template <typename T, bool VEC>
-__device__ __forceinline__ void load16(const T* p, int n, float (&v)[16]) {
-  if (VEC && n >= 16) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// 16 consecutive elements of a row as stored; those past n are 0
+template <typename T>
+struct Fp8Raw {
+  uint4 q[sizeof(T)];
+  // lo, hi: the matrix' first byte and the one after its last
+  template <bool VEC>
+  __device__ __forceinline__ void load(const T* p, int n, const uint8_t* lo, const uint8_t* hi) {
+    constexpr int S = (int)sizeof(T);
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+    if (VEC && n >= 16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) unpack2<T>(w[i], v[2 * i], v[2 * i + 1]);
-    } else {
+      for (int i = 0; i < S; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    } else if (!VEC && n >= 16 && base >= lo && base + 16 * (S + 1) <= hi) {
+      // the aligned vectors around them, shifted into place word by word and,
+      // for 16-bit elements, by half a word
+      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+      uint32_t w[4 * (S + 1)];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p) + i);
-        v[4 * i] = a.x;
-        v[4 * i + 1] = a.y;
-        v[4 * i + 2] = a.z;
-        v[4 * i + 3] = a.w;
+      for (int i = 0; i <= S; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(base) + i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
       }
-    }
-  } else {
+      if (off & 8) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+        for (int i = 0; i < 4 * S + 2; ++i) w[i] = w[i + 2];
+      }
+      if (off & 4) {
+#pragma unroll
+        for (int i = 0; i < 4 * S + 1; ++i) w[i] = w[i + 1];
+      }
+      if constexpr (S == 2) {
+#pragma unroll
+        for (int i = 0; i < 4 * S; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < S; ++i) q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+      uint32_t w[4 * sizeof(T)];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          w[i] = i < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : 0u;
+        } else {
+          const uint32_t u = i < n ? __ldg(reinterpret_cast<const uint16_t*>(p) + i) : 0u;
+          w[i / 2] = (i & 1) ? w[i / 2] | (u << 16) : u;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T); ++i) q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
   }
-}
+  // bits of the largest magnitude as fp32 (magnitudes are in the order of their
+  // bits, NaN above infinity; 16-bit ones two at a time)
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) {
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = sizeof(T) == 4 ? max(m, w[k] & 0x7FFFFFFFu) : __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+    }
+    if constexpr (sizeof(T) == 2) {
+      float lo, hi;
+      m = max(m & 0xFFFFu, m >> 16);
+      unpack2<T>(m, lo, hi);
+      m = __float_as_uint(lo);
+    }
+    return m;
+  }
+  __device__ __forceinline__ void values(float (&v)[16]) const {
+    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) unpack_vec<T, V>(q[i], *reinterpret_cast<float(*)[V]>(&v[i * V]));
+  }
+};
 
 struct Fp8EncodeParams {
   const void* x;
@@ -84,217 +155,247 @@ struct Fp8EncodeParams {
   int mma, tile, transpose;
 };
 
-// Row blocks.  A warp takes the four blocks (512 columns) of word `ka` of one
-// row; with the MMA layout also the padding rows up to a multiple of 128,
-// whose words it zeroes.
+// Row blocks.  A warp takes up to `seg` words (a word: the four blocks of 512
+// columns) of one row, the next word's loads ahead of this one's work; with
+// the MMA layout also the padding rows up to a multiple of 128, whose words it
+// zeroes.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) fp8_encode_rows_kernel(const Fp8EncodeParams p, int64_t words, uint64_t rcp_ka,
-                                                              int atoms_k) {
+__global__ void __launch_bounds__(256) fp8_encode_rows_kernel(const Fp8EncodeParams p, int64_t tasks, uint64_t rcp_nseg,
+                                                              int nseg, int seg, int words) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t nwarps = (int64_t)gridDim.x * 8;
-  const int nblk = (int)((p.cols + 127) >> 7);
-  const int64_t cols16 = (p.cols + 15) & ~int64_t(15);
+  const int cols = (int)p.cols, nblk = (cols - 1) / 128 + 1;
+  const uint8_t* lo = reinterpret_cast<const uint8_t*>(p.x);
+  const uint8_t* hi = lo + ((p.rows - 1) * p.ldx + p.cols) * sizeof(T);
   bool bad = false;
-  for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < words; it += nwarps) {
-    const int64_t row = div_rcp(it, rcp_ka);
-    const int ka = (int)(it - row * atoms_k);
-    const int64_t c0 = (int64_t)ka * 512 + lane * 16;
-    const bool live = row < p.rows;
-    float v[16];
-    const int n = live ? (int)max((int64_t)0, min((int64_t)16, p.cols - c0)) : 0;
-    if (n > 0) {
-      load16<T, VEC>(reinterpret_cast<const T*>(p.x) + row * p.ldx + c0, n, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < tasks; it += nwarps) {
+    const int64_t row = div_rcp(it, rcp_nseg);
+    const int k0 = (int)(it - row * nseg) * seg, k1 = min(k0 + seg, words);
+    int c = k0 * 512 + lane * 16;
+    // scale byte of this lane's block: MMA 512 bytes a word, linear 4
+    uint8_t* sc = p.mma ? p.scales + fp8_mma_offset(row, (int64_t)k0 * 4 + (lane >> 3), words)
+                        : p.scales + row * nblk + k0 * 4 + (lane >> 3);
+    if (row >= p.rows) {
+      for (int k = k0; k < k1; ++k, sc += 512)
+        if ((lane & 7) == 0) *sc = 0;
+      continue;
     }
-    uint32_t m = 0;
+    const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx + c;
+    uint8_t* out = p.codes + row * p.ldc + c;
+    Fp8Raw<T> next;
+    next.template load<VEC>(x, cols - c, lo, hi);
+    for (int k = k0; k < k1; ++k) {
+      const Fp8Raw<T> raw = next;
+      const int n = cols - c;
+      x += 512;
+      c += 512;
+      if (k + 1 < k1) next.template load<VEC>(x, cols - c, lo, hi);
+      uint32_t m = raw.amax_bits();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const uint32_t byte = fp8_scale_byte(m);
-    bad |= byte == 255u;
-    if (live && c0 < cols16) {
-      uint4 q;
-      q.x = fp8_codes4(v[0], v[1], v[2], v[3], byte);
-      q.y = fp8_codes4(v[4], v[5], v[6], v[7], byte);
-      q.z = fp8_codes4(v[8], v[9], v[10], v[11], byte);
-      q.w = fp8_codes4(v[12], v[13], v[14], v[15], byte);
-      *reinterpret_cast<uint4*>(p.codes + row * p.ldc + c0) = q;
-    }
-    const int blk = ka * 4 + (lane >> 3);
-    if (p.mma) {
-      const uint32_t mine = live && blk < nblk ? byte : 0u;
-      uint32_t w = __shfl_sync(0xffffffffu, mine, 0);
-      w |= __shfl_sync(0xffffffffu, mine, 8) << 8;
-      w |= __shfl_sync(0xffffffffu, mine, 16) << 16;
-      w |= __shfl_sync(0xffffffffu, mine, 24) << 24;
-      if (lane == 0) *reinterpret_cast<uint32_t*>(p.scales + fp8_mma_offset(row, (int64_t)ka * 4, atoms_k)) = w;
-    } else if ((lane & 7) == 0 && blk < nblk) {
-      p.scales[row * nblk + blk] = (uint8_t)byte;
+      for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const uint32_t byte = fp8_scale_byte(m);
+      bad |= byte == 255u;
+      float v[16];
+      raw.values(v);
+      if (n > 0) *reinterpret_cast<uint4*>(out) = fp8_codes16(v, fp8_inv2(byte), n);
+      if ((lane & 7) == 0) {
+        if (k * 4 + (lane >> 3) < nblk)
+          *sc = (uint8_t)byte;
+        else if (p.mma)
+          *sc = 0;
+      }
+      out += 512;
+      sc += p.mma ? 512 : 4;
     }
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(KL_DEVERR_NONFINITE);
 }
 
-// One 128 x 128 tile of x a CTA, staged in shared memory as it is stored.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) fp8_encode_tile_kernel(const Fp8EncodeParams p, int tiles_c) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  T* tile = reinterpret_cast<T*>(smem_raw);  // [128][128]
-  __shared__ uint32_t colmax[4][128];
-  __shared__ uint32_t warpmax[8];
-  __shared__ uint8_t row_byte[128];  // scale byte of each encoded row
+// x^T: 128 rows x 2 PAIRS columns of x a CTA.  A thread reads two columns of
+// 16 rows and writes 16 bytes of both columns' rows of x^T; the amax of a
+// column, or of the whole tile, goes through shared memory.
+template <typename T, bool VEC, int PAIRS, bool TILE>
+__global__ void __launch_bounds__(8 * PAIRS) fp8_encode_columns_kernel(const Fp8EncodeParams p, int tiles_c) {
+  static_assert(!TILE || PAIRS == 64, "a tile is 128 columns");
+  __shared__ uint32_t colmax[TILE ? 1 : 8][2 * PAIRS];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;
-  const int64_t r0 = tr * 128, c0 = tc * 128;
-  const T* x = reinterpret_cast<const T*>(p.x);
-  constexpr int E = 16 / sizeof(T);      // elements of a 16-byte vector
-  constexpr int VPR = 128 / E;           // vectors of a tile row
-  uint32_t m = 0;
-#pragma unroll 4
-  for (int i = tid; i < 128 * VPR; i += 256) {
-    const int r = i / VPR, c = (i % VPR) * E;
-    alignas(16) T v[E];
-    const int64_t left = r0 + r < p.rows ? p.cols - c0 - c : 0;
-    if (VEC && left >= E) {
-      *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(x + (r0 + r) * p.ldx + c0 + c));
-    } else {
+  // a warp: 8 pairs of 64 rows, so both its reads and its writes are whole sectors
+  constexpr int WP = PAIRS / 8;
+  const int tid = threadIdx.x, pair = (tid & 7) + tid / 32 % WP * 8, q = (tid >> 3 & 3) + tid / (32 * WP) * 4;
+  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+  const int64_t r0 = tr * 128 + q * 16, c0 = tc * (2 * PAIRS) + 2 * pair;
+  const int nr = (int)max((int64_t)0, min((int64_t)16, p.rows - r0));
+  const bool ca = c0 < p.cols, cb = c0 + 1 < p.cols;
+  const T* x = reinterpret_cast<const T*>(p.x) + r0 * p.ldx + c0;
+  float a[16], b[16];
+  uint32_t ma = 0, mb = 0;
+  if (VEC && cb && nr == 16) {  // (every load before the first use)
+    using W = std::conditional_t<sizeof(T) == 2, uint32_t, float2>;
+    W w[16];
 #pragma unroll
-      for (int j = 0; j < E; ++j) v[j] = j < left ? x[(r0 + r) * p.ldx + c0 + c + j] : from_f32<T>(0.f);
-    }
-    if (p.tile) {
+    for (int i = 0; i < 16; ++i) w[i] = __ldg(reinterpret_cast<const W*>(x + i * p.ldx));
 #pragma unroll
-      for (int j = 0; j < E; ++j) m = max(m, __float_as_uint(to_f32(v[j])) & 0x7FFFFFFFu);
-    }
-    *reinterpret_cast<uint4*>(tile + r * 128 + c) = *reinterpret_cast<const uint4*>(v);
-  }
-  m = __reduce_max_sync(0xffffffffu, m);
-  if (lane == 0) warpmax[warp] = m;
-  __syncthreads();
-  if (p.tile) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, warpmax[i]);
-  }
-  // rows and columns of the encoded matrix (x or its transpose), this tile's origin in it
-  const int64_t orows = p.transpose ? p.cols : p.rows, ocols = p.transpose ? p.rows : p.cols;
-  const int64_t or0 = p.transpose ? c0 : r0, oc0 = p.transpose ? r0 : c0;
-  const int64_t ocols16 = (ocols + 15) & ~int64_t(15);
-  bool bad = false;
-  if (p.transpose) {
-    // column pair (of 64) and row quarter of this thread
-    const int pair = (warp & 1) * 32 + lane, q = warp >> 1;
-    float a[32], b[32];
-    uint32_t ma = 0, mb = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16; ++i) {
       if constexpr (sizeof(T) == 2) {
-        unpack2<T>(*reinterpret_cast<const uint32_t*>(tile + (q * 32 + i) * 128 + 2 * pair), a[i], b[i]);
+        unpack2<T>(w[i], a[i], b[i]);
       } else {
-        const float2 w = *reinterpret_cast<const float2*>(tile + (q * 32 + i) * 128 + 2 * pair);
-        a[i] = w.x;
-        b[i] = w.y;
+        a[i] = w[i].x;
+        b[i] = w[i].y;
       }
-      ma = max(ma, __float_as_uint(a[i]) & 0x7FFFFFFFu);
-      mb = max(mb, __float_as_uint(b[i]) & 0x7FFFFFFFu);
-    }
-    if (!p.tile) {
-      colmax[q][2 * pair] = ma;
-      colmax[q][2 * pair + 1] = mb;
-      __syncthreads();
-      ma = max(max(colmax[0][2 * pair], colmax[1][2 * pair]), max(colmax[2][2 * pair], colmax[3][2 * pair]));
-      mb = max(max(colmax[0][2 * pair + 1], colmax[1][2 * pair + 1]),
-               max(colmax[2][2 * pair + 1], colmax[3][2 * pair + 1]));
-    } else {
-      ma = mb = m;
-    }
-    const uint32_t sa = fp8_scale_byte(ma), sb = fp8_scale_byte(mb);
-    bad = sa == 255u || sb == 255u;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t oc = oc0 + q * 32 + h * 16;
-      if (oc >= ocols16) continue;
-      uint32_t wa[4], wb[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = h * 16 + j * 4;
-        wa[j] = fp8_codes4(a[i], a[i + 1], a[i + 2], a[i + 3], sa);
-        wb[j] = fp8_codes4(b[i], b[i + 1], b[i + 2], b[i + 3], sb);
-      }
-      const int64_t orow = or0 + 2 * pair;
-      if (orow < orows)
-        *reinterpret_cast<uint4*>(p.codes + orow * p.ldc + oc) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-      if (orow + 1 < orows)
-        *reinterpret_cast<uint4*>(p.codes + (orow + 1) * p.ldc + oc) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
-    }
-    if (q == 0) {
-      row_byte[2 * pair] = (uint8_t)sa;
-      row_byte[2 * pair + 1] = (uint8_t)sb;
     }
   } else {
-    const uint32_t s = fp8_scale_byte(m);
-    bad = s == 255u;
-#pragma unroll 2
-    for (int i = tid; i < 128 * 8; i += 256) {
-      const int r = i >> 3, c = (i & 7) * 16;
-      if (r0 + r >= p.rows || c0 + c >= ocols16) continue;
-      uint32_t w[4];
+    T w[16], v[16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const T* t = tile + r * 128 + c + 4 * j;
-        w[j] = fp8_codes4(to_f32(t[0]), to_f32(t[1]), to_f32(t[2]), to_f32(t[3]), s);
-      }
-      *reinterpret_cast<uint4*>(p.codes + (r0 + r) * p.ldc + c0 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 16; ++i) {
+      w[i] = i < nr && ca ? x[i * p.ldx] : from_f32<T>(0.f);
+      v[i] = i < nr && cb ? x[i * p.ldx + 1] : from_f32<T>(0.f);
     }
-    if (tid < 128) row_byte[tid] = (uint8_t)s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      a[i] = to_f32(w[i]);
+      b[i] = to_f32(v[i]);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    ma = max(ma, __float_as_uint(a[i]) & 0x7FFFFFFFu);
+    mb = max(mb, __float_as_uint(b[i]) & 0x7FFFFFFFu);
+  }
+  if constexpr (TILE) {
+    ma = __reduce_max_sync(0xffffffffu, max(ma, mb));
+    if ((tid & 31) == 0) colmax[0][tid >> 5] = ma;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PAIRS / 4; ++i) ma = max(ma, colmax[0][i]);
+    mb = ma;
+  } else {
+    *reinterpret_cast<uint2*>(&colmax[q][2 * pair]) = make_uint2(ma, mb);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint2 m = *reinterpret_cast<const uint2*>(&colmax[i][2 * pair]);
+      ma = max(ma, m.x);
+      mb = max(mb, m.y);
+    }
+  }
+  const uint32_t sa = fp8_scale_byte(ma), sb = fp8_scale_byte(mb);
+  if (nr > 0) {  // at most 15 columns past the last row
+    uint8_t* out = p.codes + c0 * p.ldc + r0;
+    if (ca) *reinterpret_cast<uint4*>(out) = fp8_codes16(a, fp8_inv2(sa), nr);
+    if (cb) *reinterpret_cast<uint4*>(out + p.ldc) = fp8_codes16(b, fp8_inv2(sb), nr);
+  }
+  // scale bytes of this block of x^T's rows, by the first rows' threads; the last
+  // block of a row zeroes the unused bytes of its word, the last columns' CTA
+  // the rows up to a multiple of 128
+  const int64_t nblk = (p.rows + 127) >> 7;
+  if (p.mma) {
+    const int64_t atoms_k = (nblk + 3) >> 2;
+    auto put = [&](int64_t row, uint32_t byte) {
+      uint8_t* dst = p.scales + fp8_mma_offset(row, tr, atoms_k);
+      dst[0] = (uint8_t)byte;
+      if (tr == nblk - 1)
+        for (int64_t k = 1; ((tr + k) & 3) != 0; ++k) dst[k] = 0;
+    };
+    if (q == 0) {
+      put(c0, ca ? sa : 0u);
+      put(c0 + 1, cb ? sb : 0u);
+    }
+    if (PAIRS < 64 && tc == tiles_c - 1) {
+      const int64_t row = tiles_c * (2 * PAIRS) + tid;
+      if (row < (p.cols + 127) / 128 * 128) put(row, 0u);
+    }
+  } else if (TILE) {
+    if (tid == 0) p.scales[tc * nblk + tr] = (uint8_t)sa;
+  } else if (q == 0) {
+    if (ca) p.scales[c0 * nblk + tr] = (uint8_t)sa;
+    if (cb) p.scales[(c0 + 1) * nblk + tr] = (uint8_t)sb;
+  }
+  const bool bad = sa == 255u || sb == 255u;
+  if (__any_sync(0xffffffffu, bad) && (tid & 31) == 0) record_error(KL_DEVERR_NONFINITE);
+}
+
+// Tile blocks: one 128 x 128 tile of x a CTA, in registers (16 columns of four
+// rows a thread).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) fp8_encode_tile_kernel(const Fp8EncodeParams p, int tiles_c) {
+  __shared__ uint32_t warpmax[8];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+  const int64_t r0 = tr * 128 + (tid >> 3), c0 = tc * 128 + (tid & 7) * 16;
+  const int n = (int)min((int64_t)128, p.cols - c0);  // may be negative
+  const T* x = reinterpret_cast<const T*>(p.x) + r0 * p.ldx + c0;
+  const uint8_t* lo = reinterpret_cast<const uint8_t*>(p.x);
+  const uint8_t* hi = lo + ((p.rows - 1) * p.ldx + p.cols) * sizeof(T);
+  Fp8Raw<T> raw[4];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) raw[i].template load<VEC>(x + i * 32 * p.ldx, r0 + i * 32 < p.rows ? n : 0, lo, hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, raw[i].amax_bits());
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((tid & 31) == 0) warpmax[tid >> 5] = m;
   __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, warpmax[i]);
+  const uint32_t byte = fp8_scale_byte(m);
+  const uint64_t inv2 = fp8_inv2(byte);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[16];
+    raw[i].values(v);
+    if (n > 0 && r0 + i * 32 < p.rows)
+      *reinterpret_cast<uint4*>(p.codes + (r0 + i * 32) * p.ldc + c0) = fp8_codes16(v, inv2, n);
+  }
   // scale bytes of this tile's rows; the last tile of a row block zeroes the
   // unused bytes of its words
-  const int64_t oblk = oc0 >> 7, nblk = (ocols + 127) >> 7;
-  if (tid < 128) {
-    const int64_t row = or0 + tid;
-    const uint32_t byte = row < orows ? row_byte[tid] : 0u;
-    if (p.mma) {
-      const int64_t atoms_k = (nblk + 3) >> 2;
-      uint8_t* dst = p.scales + fp8_mma_offset(row, oblk, atoms_k);
-      dst[0] = (uint8_t)byte;
-      if (oblk == nblk - 1)
-        for (int64_t k = 1; ((oblk + k) & 3) != 0; ++k) dst[k] = 0;
-    } else if (!p.tile) {
-      if (row < orows) p.scales[row * nblk + oblk] = (uint8_t)byte;
-    } else if (tid == 0) {
-      p.scales[(or0 >> 7) * nblk + oblk] = (uint8_t)byte;
+  const int64_t nblk = (p.cols + 127) >> 7;
+  if (p.mma) {
+    if (tid < 128) {
+      const int64_t row = tr * 128 + tid;
+      uint8_t* dst = p.scales + fp8_mma_offset(row, tc, (nblk + 3) >> 2);
+      dst[0] = (uint8_t)(row < p.rows ? byte : 0u);
+      if (tc == nblk - 1)
+        for (int64_t k = 1; ((tc + k) & 3) != 0; ++k) dst[k] = 0;
     }
+  } else if (tid == 0) {
+    p.scales[tr * nblk + tc] = (uint8_t)byte;
   }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(KL_DEVERR_NONFINITE);
+  if (byte == 255u && tid == 0) record_error(KL_DEVERR_NONFINITE);
+}
+
+template <typename T, int PAIRS, bool TILE>
+static cudaError_t launch_fp8_columns(const Fp8EncodeParams& p, cudaStream_t s) {
+  const int64_t tiles_c = (p.cols + 2 * PAIRS - 1) / (2 * PAIRS), tiles = (p.rows + 127) / 128 * tiles_c;
+  const bool pairs = (reinterpret_cast<uintptr_t>(p.x) % (2 * sizeof(T))) == 0 && p.ldx % 2 == 0;
+  auto kern = pairs ? fp8_encode_columns_kernel<T, true, PAIRS, TILE> : fp8_encode_columns_kernel<T, false, PAIRS, TILE>;
+  return launch_pdl(kern, dim3((unsigned)tiles), dim3(8 * PAIRS), 0, s, p, (int)tiles_c);
 }
 
 template <typename T>
 static cudaError_t launch_fp8_encode(const Fp8EncodeParams& p, cudaStream_t s) {
   const bool vec = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && (p.ldx * sizeof(T)) % 16 == 0;
   if (!p.tile && !p.transpose) {
-    const int64_t atoms_k = (p.cols + 511) / 512;
-    const int64_t words = (p.mma ? (p.rows + 127) / 128 * 128 : p.rows) * atoms_k;
-    const int64_t ctas = (words + 7) / 8, cap = (int64_t)device_sm_count() * 8;
+    const int64_t words = (p.cols + 511) / 512, rows = p.mma ? (p.rows + 127) / 128 * 128 : p.rows;
+    const int64_t cap = (int64_t)device_sm_count() * 8;
+    // up to eight words a task, fewer where that leaves warps without one
+    int64_t seg = rows * words / (cap * 8);
+    seg = seg < 1 ? 1 : seg > 8 ? 8 : seg;
+    const int64_t nseg = (words + seg - 1) / seg, tasks = rows * nseg, ctas = (tasks + 7) / 8;
+    seg = (words + nseg - 1) / nseg;
     const dim3 grid((unsigned)(ctas < cap ? ctas : cap));
-    const uint64_t r = rcp64((uint64_t)atoms_k);
-    return vec ? launch_pdl(fp8_encode_rows_kernel<T, true>, grid, dim3(256), 0, s, p, words, r, (int)atoms_k)
-               : launch_pdl(fp8_encode_rows_kernel<T, false>, grid, dim3(256), 0, s, p, words, r, (int)atoms_k);
+    auto kern = vec ? fp8_encode_rows_kernel<T, true> : fp8_encode_rows_kernel<T, false>;
+    return launch_pdl(kern, grid, dim3(256), 0, s, p, tasks, rcp64((uint64_t)nseg), (int)nseg, (int)seg, (int)words);
   }
+  if (p.transpose)  // rows of 128 bytes or more at a time
+    return p.tile ? launch_fp8_columns<T, 64, true>(p, s) : launch_fp8_columns<T, 64 / sizeof(T), false>(p, s);
   const int64_t tiles_c = (p.cols + 127) / 128, tiles = (p.rows + 127) / 128 * tiles_c;
-  const size_t smem = 128 * 128 * sizeof(T);
   auto kern = vec ? fp8_encode_tile_kernel<T, true> : fp8_encode_tile_kernel<T, false>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(kern, dim3((unsigned)tiles), dim3(256), smem, s, p, (int)tiles_c);
+  return launch_pdl(kern, dim3((unsigned)tiles), dim3(256), 0, s, p, (int)tiles_c);
 }
 
 }  // namespace kl
@@ -317,7 +418,7 @@ kl_status kl_quantize_fp8_block(const void* x, int dtype, int64_t rows, int64_t 
   if (rows < 1 || cols < 1 || rows > KL_FP8_MAX_DIM || cols > KL_FP8_MAX_DIM) return KL_ERR_UNSUPPORTED_SHAPE;
   const int64_t ocols = (flags & KL_FP8_TRANSPOSE) ? rows : cols;
   if (ldx < cols || ldc < (ocols + 15) / 16 * 16 || ldc % 16) return KL_ERR_INVALID_ARG;
-  if ((rows + 127) / 128 * ((cols + 127) / 128) > KL_FP8_MAX_DIM) return KL_ERR_UNSUPPORTED_SHAPE;
+  if ((rows + 127) / 128 * ((cols + 127) / 128) > KL_FP8_MAX_DIM / 4) return KL_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(x, dtype == KL_F32 ? 4 : 2) || !aligned(codes, 16) || !aligned(scales, 4)) return KL_ERR_MISALIGNED;
   kl_status st = check_arch();
   if (st != KL_OK) return st;

@@ -13,8 +13,8 @@
 // so positions far along an axis lose nothing; sincospif of the reduced angle
 // is fp32.  Each angle is used by every head of its token: a CTA makes the
 // table of a few tokens in shared memory, then its threads walk the (token,
-// head) rows with four rows' loads in flight.  CTAs stay for many chunks of
-// tokens; two table buffers leave one barrier a chunk.
+// head) rows, the next rows' loads ahead of this row's work.  CTAs stay for a
+// few chunks of tokens; two table buffers leave one barrier a chunk.
 //
 // Bound by HBM: one read and one write of the tensor; the fp64 work is one
 // angle per (token, pair), a head's share of it 1 / H.
@@ -28,7 +28,7 @@ namespace kl {
 
 constexpr int kRopeMaxPairs = 256;  // head dim 512
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;       // rows a thread loads before it stores the first
+constexpr int kRopeBatch = 2;       // rows a thread loads, ahead of the two it turns and stores
 constexpr int kRopeTable = 2560;    // (token, pair) entries of a table buffer: two are 40 KB
 
 struct RopeParams {
@@ -38,8 +38,8 @@ struct RopeParams {
   int64_t batch, tokens;
   int64_t xs_b, xs_t, xs_h, os_b, os_t, os_h;  // strides in elements; dims are consecutive
   int64_t pos_b;                               // position rows between batches (0: shared)
-  int64_t chunks;                              // token chunks of a batch
-  int64_t items;                               // batch * chunks * head parts
+  unsigned chunks;                             // token chunks of a batch
+  unsigned items;                              // batch * chunks * head parts
   int heads, hparts, hper;                     // a chunk's heads are in hparts parts of hper
   int dim, pairs, naxes, pos_type;
   int units;            // per head: vectors of dims (interleaved) or of pairs, then of copied dims (half)
@@ -75,19 +75,18 @@ struct RopeUnit {
       a = load_vec<T, V>(x + u * V);
     }
   }
-  __device__ __forceinline__ void store(T* o, const RopeParams& p, int u, int pair_units, const float2* row) {
+  // cs: the table's row from the unit's first pair; whole: all its dims turn
+  __device__ __forceinline__ void store(T* o, const RopeParams& p, int u, int pair_units, bool whole,
+                                        const float2* cs) {
     if constexpr (HALF || V == 1) {
-      float va[V], vc[V];
-      unpack_vec<T, V>(a, va);
-      if (u < pair_units) {
+      if (whole) {
+        float va[V], vc[V];
+        float2 t[V];
+        entries(cs, t);
+        unpack_vec<T, V>(a, va);
         unpack_vec<T, V>(c, vc);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 cs = row[u * V + i];
-          const float x0 = va[i], x1 = vc[i];
-          va[i] = x0 * cs.x - x1 * cs.y;
-          vc[i] = x0 * cs.y + x1 * cs.x;
-        }
+        for (int i = 0; i < V; ++i) turn(va[i], vc[i], t[i]);
         if constexpr (HALF) {
           store_vec<T, V>(o + u * V, va);
           store_vec<T, V>(o + p.pairs + u * V, vc);
@@ -104,16 +103,34 @@ struct RopeUnit {
     } else {
       float v[V];
       unpack_vec<T, V>(a, v);
+      if (whole) {
+        float2 t[NP];
+        entries(cs, t);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        if (u * NP + i < p.pairs) {  // dims past the pairs stay as they are
-          const float2 cs = row[u * NP + i];
-          const float x0 = v[2 * i], x1 = v[2 * i + 1];
-          v[2 * i] = x0 * cs.x - x1 * cs.y;
-          v[2 * i + 1] = x0 * cs.y + x1 * cs.x;
-        }
+        for (int i = 0; i < NP; ++i) turn(v[2 * i], v[2 * i + 1], t[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          if (u * NP + i < p.pairs) turn(v[2 * i], v[2 * i + 1], cs[i]);  // dims past the pairs stay as they are
       }
       store_vec<T, V>(o + u * V, v);
+    }
+  }
+  static __device__ __forceinline__ void turn(float& x0, float& x1, const float2& cs) {
+    const float y = x0 * cs.x - x1 * cs.y;
+    x1 = x0 * cs.y + x1 * cs.x;
+    x0 = y;
+  }
+  static __device__ __forceinline__ void entries(const float2* cs, float2 (&t)[NP]) {
+    if constexpr (NP == 1) {
+      t[0] = cs[0];
+    } else {  // table rows and units start on two entries
+#pragma unroll
+      for (int i = 0; i < NP; i += 2) {
+        const float4 f = *reinterpret_cast<const float4*>(cs + i);
+        t[i] = make_float2(f.x, f.y);
+        t[i + 1] = make_float2(f.z, f.w);
+      }
     }
   }
   // the loaded bits themselves
@@ -131,8 +148,8 @@ struct RopeUnit {
 // interleaved pairs then move two elements).  A thread keeps one unit u of the
 // head and walks the rows.
 template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_axes_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ __align__(16) float2 rope_tables[];  // [2][nt][pairs] (cos, sin)
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_axes_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) float2 rope_tables[];  // [2][nt][pairs, even] (cos, sin)
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
@@ -143,50 +160,83 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_axes_kernel(const __grid
   while (tj >= p.first[axis + 1]) ++axis;
   const int ulim = min(p.units, kRopeThreads), slots = kRopeThreads / ulim;
   const int u0 = tid % ulim, slot = tid / ulim;
-  const int pair_units = HALF || V == 1 ? p.pairs / V : 0;
+  const int pair_units = p.pairs / RopeUnit<T, V, HALF>::NP, pitch = (p.pairs + 1) & ~1;
   int buf = 0;
-  for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x, buf ^= 1) {
-    const int64_t bc = item / p.hparts, b = bc / p.chunks, t0 = (bc - b * p.chunks) * p.nt;
+  for (unsigned item = blockIdx.x; item < p.items; item += gridDim.x, buf ^= 1) {
+    const unsigned bc = p.hparts == 1 ? item : item / (unsigned)p.hparts, b = p.batch == 1 ? 0u : bc / p.chunks;
+    const int64_t t0 = (int64_t)(bc - b * p.chunks) * p.nt;
     const int h0 = (int)(item - bc * p.hparts) * p.hper, nh = min(p.hper, p.heads - h0);
     const int nt = (int)min((int64_t)p.nt, p.tokens - t0);
-    float2* table = rope_tables + buf * p.nt * p.pairs;
+    float2* table = rope_tables + buf * p.nt * pitch;
+    // the thread's rows are `slots` apart: a step of dt tokens and dh heads,
+    // and one of a token back by a turn of the heads where that passes the last
+    const int rows = slot < slots ? nt * nh : 0, dt = slots / nh, dh = slots - dt * nh, ts0 = slot / nh;
+    const int64_t xstep = dt * p.xs_t + dh * p.xs_h, xturn = p.xs_t - nh * p.xs_h;
+    const int64_t ostep = dt * p.os_t + dh * p.os_h, oturn = p.os_t - nh * p.os_h;
+    const int cstep = dt * pitch;
+    int u = u0, h = slot - ts0 * nh, r = slot;
+    const T* x = reinterpret_cast<const T*>(p.x) + b * p.xs_b + (t0 + ts0) * p.xs_t + (h0 + h) * p.xs_h;
+    T* o = reinterpret_cast<T*>(p.out) + b * p.os_b + (t0 + ts0) * p.os_t + (h0 + h) * p.os_h;
+    const float2* cs = table + ts0 * pitch;
+    RopeUnit<T, V, HALF> next[kRopeBatch];
+    T* nout[kRopeBatch];
+    const float2* ncs[kRopeBatch];
+    auto fetch = [&] {  // the next rows' loads (those past the last are not made)
+#pragma unroll
+      for (int k = 0; k < kRopeBatch; ++k) {
+        nout[k] = o;
+        ncs[k] = cs;
+        if (r < rows) next[k].load(x, p, u, pair_units);
+        r += slots;
+        x += xstep;
+        o += ostep;
+        cs += cstep;
+        h += dh;
+        if (h >= nh) {
+          h -= nh;
+          x += xturn;
+          o += oturn;
+          cs += pitch;
+        }
+      }
+    };
+    fetch();  // under way while the table is made
     if (ts < tslots) {
       for (int t = ts; t < nt; t += tslots) {
-        const double h = rope_pos(p, (b * p.pos_b + t0 + t) * p.naxes + axis) * freq;
-        float sn, cs;
-        sincospif((float)(h - 2.0 * rint(0.5 * h)), &sn, &cs);
-        table[t * p.pairs + tj] = make_float2(cs, p.sign * sn);
+        const double a = rope_pos(p, (b * p.pos_b + t0 + t) * p.naxes + axis) * freq;
+        float sn, c;
+        sincospif((float)(a - 2.0 * rint(0.5 * a)), &sn, &c);
+        table[t * pitch + tj] = make_float2(c, p.sign * sn);
       }
     }
     __syncthreads();
-    if (slot >= slots) continue;
-    const T* x = reinterpret_cast<const T*>(p.x) + b * p.xs_b + t0 * p.xs_t + h0 * p.xs_h;
-    T* o = reinterpret_cast<T*>(p.out) + b * p.os_b + t0 * p.os_t + h0 * p.os_h;
-    const int rows = nt * nh, dt = slots / nh, dh = slots - dt * nh;  // a step of `slots` rows
-    for (int u = u0; u < p.units; u += kRopeThreads) {
-      int t = slot / nh, h = slot - t * nh;
-      for (int r = slot; r < rows; r += kRopeBatch * slots) {
-        // several rows' loads ahead of the first store: x and out may be the
-        // same tensor, so the compiler cannot move them itself
+    while (true) {
+      for (int done = slot; done < rows; done += kRopeBatch * slots) {
         RopeUnit<T, V, HALF> q[kRopeBatch];
-        int tt[kRopeBatch], hh[kRopeBatch];
+        T* out[kRopeBatch];
+        const float2* row[kRopeBatch];
 #pragma unroll
         for (int k = 0; k < kRopeBatch; ++k) {
-          tt[k] = t;
-          hh[k] = h;
-          if (r + k * slots < rows) q[k].load(x + t * p.xs_t + h * p.xs_h, p, u, pair_units);
-          t += dt;
-          h += dh;
-          if (h >= nh) {
-            h -= nh;
-            ++t;
-          }
+          q[k] = next[k];
+          out[k] = nout[k];
+          row[k] = ncs[k];
         }
+        // x and out may be the same tensor: the compiler cannot move these
+        // loads above the stores itself
+        fetch();
 #pragma unroll
         for (int k = 0; k < kRopeBatch; ++k)
-          if (r + k * slots < rows)
-            q[k].store(o + tt[k] * p.os_t + hh[k] * p.os_h, p, u, pair_units, table + tt[k] * p.pairs);
+          if (done + k * slots < rows)
+            q[k].store(out[k], p, u, pair_units, u < pair_units, row[k] + u * RopeUnit<T, V, HALF>::NP);
       }
+      if ((u += kRopeThreads) >= p.units) break;
+      // (heads of more than 256 units, which single elements can have: again from the first row)
+      h = slot - ts0 * nh;
+      r = slot;
+      x = reinterpret_cast<const T*>(p.x) + b * p.xs_b + (t0 + ts0) * p.xs_t + (h0 + h) * p.xs_h;
+      o = reinterpret_cast<T*>(p.out) + b * p.os_b + (t0 + ts0) * p.os_t + (h0 + h) * p.os_h;
+      cs = table + ts0 * pitch;
+      fetch();
     }
   }
 }
@@ -194,17 +244,21 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_axes_kernel(const __grid
 template <typename T, int V>
 static cudaError_t launch_rope_v(RopeParams& p, bool half, cudaStream_t s) {
   p.units = half ? p.pairs / V + (p.dim - 2 * p.pairs) / V : (V == 1 ? (p.dim + 1) / 2 : p.dim / V);
-  // chunks of about 24 KB of x, within the table; smaller ones, then parts of
-  // the heads, where that leaves fewer than four a SM
-  const int64_t want = (int64_t)device_sm_count() * 4, total = p.batch * p.tokens;
-  const int64_t token_bytes = (int64_t)p.heads * p.dim * sizeof(T);
-  int64_t nt = 24576 / token_bytes, most = kRopeTable / p.pairs;
-  if (nt > total / want) nt = total / want;
-  if (nt > most) nt = most;
-  if (nt > p.tokens) nt = p.tokens;
-  if (nt < 1) nt = 1;
+  // Three CTAs a SM, each of one or a few chunks of tokens within the table:
+  // the chunk that leaves the most loaded CTA the fewest tokens.  Fewer tokens
+  // than CTAs: one each, and parts of the heads.
+  const int64_t want = (int64_t)device_sm_count() * 3;
+  const int64_t most = kRopeTable / (p.pairs + 1);
+  int64_t nt = 1, least = INT64_MAX;
+  for (int64_t c = most < p.tokens ? most : p.tokens; c >= 1; --c) {
+    const int64_t n = p.batch * ((p.tokens + c - 1) / c), load = (n + want - 1) / want * c;
+    if (load < least) {
+      least = load;
+      nt = c;
+    }
+  }
   p.nt = (int)nt;
-  p.chunks = (p.tokens + nt - 1) / nt;
+  p.chunks = (unsigned)((p.tokens + nt - 1) / nt);
   const int ulim = p.units < kRopeThreads ? p.units : kRopeThreads, slots = kRopeThreads / ulim;
   int64_t parts = want / (p.batch * p.chunks);
   const int64_t hchunks = (p.heads + slots - 1) / slots;  // no part without a row for every slot
@@ -212,9 +266,9 @@ static cudaError_t launch_rope_v(RopeParams& p, bool half, cudaStream_t s) {
   if (parts < 1) parts = 1;
   p.hper = (int)((p.heads + parts - 1) / parts);
   p.hparts = (p.heads + p.hper - 1) / p.hper;
-  p.items = p.batch * p.chunks * p.hparts;
-  const unsigned grid = (unsigned)(p.items < want ? p.items : want);
-  const size_t smem = (size_t)2 * nt * p.pairs * sizeof(float2);
+  p.items = (unsigned)(p.batch * p.chunks * p.hparts);
+  const unsigned grid = p.items < (unsigned)want ? p.items : (unsigned)want;
+  const size_t smem = (size_t)2 * nt * ((p.pairs + 1) & ~1) * sizeof(float2);
   return half ? launch_pdl(rope_axes_kernel<T, V, true>, dim3(grid), dim3(kRopeThreads), smem, s, p)
               : launch_pdl(rope_axes_kernel<T, V, false>, dim3(grid), dim3(kRopeThreads), smem, s, p);
 }

@@ -650,7 +650,7 @@ kl_status kl_dit_step_cached(const kl_dit_shape* shape, const kl_dit_weights* w,
  */
 #define KL_FP8_TILE 16
 #define KL_FP8_TRANSPOSE 32
-#define KL_FP8_MAX_DIM 0x7FFFFFFF /* rows, cols, and 128 x 128 tiles */
+#define KL_FP8_MAX_DIM 0x40000000 /* rows, cols; four times the 128 x 128 tiles */
 size_t kl_fp8_scales_bytes(int64_t rows, int64_t cols, int flags); /* of the encoded matrix */
 kl_status kl_quantize_fp8_block(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, void* codes,
                                 int64_t ldc, void* scales, int flags, void* stream);
