@@ -9,12 +9,13 @@ library is missing every call raises.
 """
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass
 
 import torch
 
-from .build import LIB_PATH
+from .build import BIND_PATH, LIB_PATH
 
 __all__ = [
     "KLError", "lib", "NVFP4", "quantize_nvfp4", "ln_modulate_quantize_nvfp4", "gemm_nvfp4_fused",
@@ -677,69 +678,37 @@ def dit_step_cached(shape, weights, cache, threshold, latent, text, mod_mode, mo
 
 # ------------------------------------------- the eight-bit projection path
 # These calls run on the current stream of their tensors' device, whichever
-# device is current, and allocate outputs and scratch per call.
+# device is current, and allocate outputs and scratch per call.  They go
+# through the compiled binding: from here they would cost more of the CPU than
+# the small ones take on the GPU.
 KL_FP8_TILE, KL_FP8_TRANSPOSE = 16, 32
-_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
-_POS_TYPE = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
-_OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
-_U8, _F32 = (torch.uint8,), (torch.float32,)
-_PAIRING, _LADDER = {"interleaved": 0, "half": 1}, {"axis": 0, "shared": 2}
-_I64x3, _I64x4 = ctypes.c_int64 * 3, ctypes.c_int64 * 4
 FP8_GEMM_KERNELS = {"auto": 0, "pair_256x256": 1, "pair_256x128": 2, "split": 3}
+_OUT_TYPE = {torch.bfloat16: KL_OUT_BF16, torch.float32: KL_OUT_F32}
+_BLOCK, _LAYOUT = {"row": 0, "tile": KL_FP8_TILE}, {"mma": KL_SCALE_MMA, "linear": 0}
+_PAIRING, _LADDER = {"interleaved": 0, "half": 1}, {"axis": 0, "shared": 2}
+_EXT = None
 
 
-# The small calls are bound by this file's own work (a launch is about 4 us of
-# the CPU, torch.empty 1.3 to 2.3, a torch.cuda.Stream object 3), so it asks
-# for the raw stream and makes its tensors the cheapest way.
-def _call(device, name, *args):
-    """Call an entry point whose last argument is the stream, on ``device`` (a
-    tensor's: its index is known)."""
-    fn, index = getattr(_LIB or lib(), name), device.index
-    if index == torch._C._cuda_getDevice():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status != KL_OK:
-        raise KLError(status, name)
-
-
-def _need_on(t, device, dtypes, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected a CUDA tensor of {' / '.join(str(d) for d in dtypes)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
+def _ext():
+    """The compiled binding klein_torch.so (raises if it has not been built)."""
+    global _EXT
+    if _EXT is None:
+        lib()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError(f"{BIND_PATH} is missing: build it with "
+                               "`python -m diffusion_transformer_image_nvfp4_b200.build`")
+        spec = importlib.util.spec_from_file_location("klein_torch", BIND_PATH)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        ext.set_error(KLError)
+        _EXT = ext
+    return _EXT
 
 
 def _rows(t, name):
     """(rows, cols, row stride) of ``t`` [..., cols] as a matrix whose rows lie
     at one stride; raises if it is not one (no copy is made)."""
-    shape = t.shape
-    n = t.numel()
-    if not shape or n == 0:
-        raise ValueError(f"{name}: expected a tensor [..., cols] that is not empty")
-    cols = shape[-1]
-    if t.is_contiguous():
-        return n // cols, cols, cols
-    if cols > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be consecutive")
-    rows, ld = 1, cols
-    for n, st in reversed(list(zip(shape[:-1], t.stride()[:-1]))):
-        if n == 1:
-            continue
-        if rows == 1:
-            ld = st
-        elif st != rows * ld:
-            raise ValueError(f"{name}: rows must lie at one stride")
-        rows *= n
-    if ld < cols:
-        raise ValueError(f"{name}: rows must not overlap")
-    return rows, cols, ld
-
-
-def _like(t):
-    """An uninitialised contiguous tensor of t's shape and type."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return _ext().rows(t, name)
 
 
 @dataclass
@@ -755,39 +724,14 @@ class FP8Block:
     layout: str = "mma"
     block: str = "row"
 
-    def abi(self, device, name):
-        """The checked operand of kl_gemm_fp8_block on ``device``."""
-        codes, scales, rows, cols = self.codes, self.scales, self.rows, self.cols
-        _need_on(codes, device, _U8, name)
-        _need_on(scales, device, _U8, name)
-        shape, ld = codes.shape, codes.stride()
-        if len(shape) != 2 or shape[0] < rows or shape[1] < cols or ld[1] != 1:
-            raise ValueError(f"{name}.codes: expected [rows, >= cols] with consecutive columns")
-        if not scales.is_contiguous() or scales.numel() < (rows + 127) // 128 * ((cols + 511) // 512) * 512:
-            raise ValueError(f"{name}.scales: too small for [{rows}, {cols}]")
-        return _FP8Tensor(codes.data_ptr(), scales.data_ptr(), ld[0])
-
 
 def quantize_fp8_block(x, block="row", transpose=False, layout="mma"):
     """kl_quantize_fp8_block of ``x`` [..., cols] (bf16, fp16 or fp32 CUDA
     tensor; leading dimensions are rows), or of its transpose: an FP8Block."""
-    _need_on(x, None, _DTYPE, "x")
-    if block not in ("row", "tile") or layout not in ("mma", "linear"):
+    if block not in _BLOCK or layout not in _LAYOUT:
         raise ValueError('block: "row" or "tile"; layout: "mma" or "linear"')
-    R, C, ld = _rows(x, "x")
-    rows, cols = (C, R) if transpose else (R, C)
-    flags = (KL_SCALE_MMA if layout == "mma" else 0) | (KL_FP8_TILE if block == "tile" else 0) | (
-        KL_FP8_TRANSPOSE if transpose else 0)
-    ldc, blocks = (cols + 15) // 16 * 16, (cols + 127) // 128
-    device = x.device
-    codes = torch.empty((rows, ldc), dtype=torch.uint8, device=device)
-    if layout == "mma":
-        scales = torch.empty((rows + 127) // 128 * ((blocks + 3) // 4) * 512, dtype=torch.uint8, device=device)
-    else:
-        scales = torch.empty(((rows + 127) // 128 if block == "tile" else rows, blocks), dtype=torch.uint8,
-                             device=device)
-    _call(device, "kl_quantize_fp8_block", x.data_ptr(), _DTYPE[x.dtype], R, C, ld, codes.data_ptr(), ldc,
-          scales.data_ptr(), flags)
+    flags = _BLOCK[block] | _LAYOUT[layout] | (KL_FP8_TRANSPOSE if transpose else 0)
+    codes, scales, rows, cols = (_EXT or _ext()).quantize(x, flags)
     return FP8Block(codes, scales, rows, cols, layout, block)
 
 
@@ -797,21 +741,10 @@ def gemm_fp8_block(A, W, out=None, out_dtype=torch.bfloat16, kernel="auto"):
     its rows at any stride.  ``kernel``: "auto" or one of FP8_GEMM_KERNELS."""
     if A.layout != "mma" or W.layout != "mma" or A.cols != W.cols:
         raise ValueError("operands must share K and use the MMA scale layout")
-    device = A.codes.device
-    a, w = A.abi(device, "A"), W.abi(device, "W")
-    M, N, K = A.rows, W.rows, A.cols
-    if out is None:
-        if out_dtype not in _OUT_TYPE:
-            raise ValueError("out_dtype: bfloat16 or float32")
-        out, ldo = torch.empty((M, N), dtype=out_dtype, device=device), N
-    else:
-        _need_on(out, device, _OUT_TYPE, "out")
-        if tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
-            raise ValueError(f"out: expected [{M}, {N}] with consecutive columns")
-        out_dtype, ldo = out.dtype, max(out.stride(0), N)
-    _call(device, "kl_gemm_fp8_block", ctypes.byref(a), ctypes.byref(w), M, N, K, out.data_ptr(),
-          _OUT_TYPE[out_dtype], ldo, FP8_GEMM_KERNELS[kernel])
-    return out
+    if out_dtype not in _OUT_TYPE:
+        raise ValueError("out_dtype: bfloat16 or float32")
+    return (_EXT or _ext()).gemm(A.codes, A.scales, A.rows, W.codes, W.scales, W.rows, A.cols, out,
+                                 _OUT_TYPE[out_dtype], FP8_GEMM_KERNELS[kernel])
 
 
 def rope_axes(x, pos, sections, theta=10000.0, pairing="interleaved", ladder="axis", inverse=False, out=None):
@@ -821,59 +754,11 @@ def rope_axes(x, pos, sections, theta=10000.0, pairing="interleaved", ladder="ax
     per axis.  ``pairing``: "interleaved" (2j, 2j + 1) or "half" (j, j + P);
     ``ladder``: "axis" or "shared".  ``inverse`` turns back: the gradient.
     ``out``: a tensor of x's shape and type, or ``x`` itself (in place)."""
-    _need_on(x, None, _DTYPE, "x")
-    device, shape, xs = x.device, x.shape, x.stride()
-    _need_on(pos, device, _POS_TYPE, "pos")
-    if len(shape) not in (3, 4) or x.numel() == 0 or (shape[-1] > 1 and xs[-1] != 1):
-        raise ValueError("x: expected [tokens, heads, dim] or [batch, tokens, heads, dim], dims consecutive")
-    flags = _PAIRING.get(pairing, 8) | _LADDER.get(ladder, 8) | (4 if inverse else 0)
-    if flags & 8:
+    if pairing not in _PAIRING or ladder not in _LADDER:
         raise ValueError('pairing: "interleaved" or "half"; ladder: "axis" or "shared"')
-    four = len(shape) == 4
-    batch = shape[0] if four else 1
-    tokens, heads, dim = shape[-3:]
-    naxes = len(sections)
-    pshape = pos.shape
-    shared = pshape == (tokens, naxes)
-    if not 1 <= naxes <= 4 or not (shared or (four and pshape == (batch, tokens, naxes))):
-        raise ValueError(f"pos: expected [{tokens}, {naxes}] or [{batch}, {tokens}, {naxes}], 1 to 4 axes")
-    pos = pos.contiguous()
-    if out is None:
-        out = _like(x)
-        os = (tokens * heads * dim, heads * dim, dim)
-    else:
-        _need_on(out, device, (x.dtype,), "out")
-        os = out.stride()
-        if out.shape != shape or (dim > 1 and os[-1] != 1) or any(n > 1 and st == 0 for n, st in zip(shape, os)):
-            raise ValueError("out: expected x's shape, dims consecutive, no broadcast dimensions")
-        os = os[:3] if four else (0, *os[:2])
-    args = _RopeArgs(x.data_ptr(), out.data_ptr(), pos.data_ptr(), _DTYPE[x.dtype], _POS_TYPE[pos.dtype], shared,
-                     flags, naxes, _I64x4(*sections), batch, tokens, heads, dim,
-                     _I64x3(*(xs[:3] if four else (0, *xs[:2]))), _I64x3(*os), theta)
-    _call(device, "kl_rope_axes", ctypes.byref(args))
-    return out
-
-
-def _ln_params(rows, cols, device, params, groups):
-    """(groups, dtype code) of gain / bias tensors [cols] or [groups, cols]."""
-    dtype = None
-    for t, n in params:
-        if t is None:
-            continue
-        _need_on(t, device, _DTYPE, n)
-        shape = t.shape
-        if not t.is_contiguous() or len(shape) not in (1, 2) or shape[-1] != cols:
-            raise ValueError(f"{n}: expected a contiguous [{cols}] or [groups, {cols}] tensor")
-        g = shape[0] if len(shape) == 2 else 1
-        if groups is not None and g != groups:
-            raise ValueError(f"{n}: {g} groups, expected {groups}")
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError("gain and bias must have one type")
-        groups, dtype = g, t.dtype
-    groups = 1 if groups is None else groups
-    if groups < 1 or rows % groups:
-        raise ValueError(f"{groups} groups do not divide {rows} rows")
-    return groups, _DTYPE[dtype] if dtype is not None else 1
+    flags = _PAIRING[pairing] | _LADDER[ladder] | (4 if inverse else 0)
+    y = (_EXT or _ext()).rope(x, pos, sections, theta, flags, out)
+    return y if out is None else out
 
 
 def layer_norm_forward(x, gain=None, bias=None, modulate=False, eps=1e-6):
@@ -881,16 +766,7 @@ def layer_norm_forward(x, gain=None, bias=None, modulate=False, eps=1e-6):
     (y, mean, rstd), mean and rstd fp32 [rows].  ``gain`` / ``bias``: [cols], or
     [groups, cols] with the rows divided evenly among the groups; ``modulate``:
     the factor is 1 + gain (adaLN)."""
-    _need_on(x, None, _DTYPE, "x")
-    R, C, ld = _rows(x, "x")
-    dtype, device = x.dtype, x.device
-    groups, ptype = _ln_params(R, C, device, ((gain, "gain"), (bias, "bias")), None)
-    y = _like(x)
-    mean = torch.empty(R, dtype=torch.float32, device=device)
-    rstd = torch.empty_like(mean)
-    _call(device, "kl_layer_norm_forward", x.data_ptr(), _DTYPE[dtype], R, C, ld, _ptr(gain), _ptr(bias), ptype,
-          groups, eps, 1 if modulate else 0, y.data_ptr(), C, mean.data_ptr(), rstd.data_ptr())
-    return y, mean, rstd
+    return (_EXT or _ext()).ln_forward(x, gain, bias, modulate, eps)
 
 
 def layer_norm_backward(dy, x, mean, rstd, gain=None, modulate=False, groups=None, param_grads=True):
@@ -898,31 +774,7 @@ def layer_norm_backward(dy, x, mean, rstd, gain=None, modulate=False, groups=Non
     rstd; dgain and dbias fp32 [groups, cols] (None without ``param_grads``).
     ``groups``: the gain's number of rows, or how many groups' sums are wanted
     when there is no gain."""
-    _need_on(x, None, _DTYPE, "x")
-    _need_on(dy, x.device, (x.dtype,), "dy")
-    if dy.shape != x.shape:
-        raise ValueError("dy and x must have one shape")
-    R, C, ld = _rows(x, "x")
-    lddy = _rows(dy, "dy")[2]
-    device = x.device
-    for t, n in ((mean, "mean"), (rstd, "rstd")):
-        _need_on(t, device, _F32, n)
-        if t.numel() != R or not t.is_contiguous():
-            raise ValueError(f"{n}: expected contiguous fp32 [{R}]")
-    groups, ptype = _ln_params(R, C, device, ((gain, "gain"),), groups)
-    dtype = _DTYPE[x.dtype]
-    dx = _like(x)
-    dgain = dbias = ws = None
-    nbytes = 0
-    if param_grads:
-        dgain = torch.empty((groups, C), dtype=torch.float32, device=device)
-        dbias = torch.empty_like(dgain)
-        nbytes = lib().kl_layer_norm_backward_workspace_size(dtype, R, C, groups)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _call(device, "kl_layer_norm_backward", dy.data_ptr(), lddy, x.data_ptr(), ld, dtype, R, C,
-          mean.data_ptr(), rstd.data_ptr(), _ptr(gain), ptype, groups, 1 if modulate else 0, dx.data_ptr(), C,
-          _ptr(dgain), _ptr(dbias), _ptr(ws), nbytes)
-    return dx, dgain, dbias
+    return (_EXT or _ext()).ln_backward(dy, x, mean, rstd, gain, modulate, groups, param_grads)
 
 
 def device_status(clear=True):

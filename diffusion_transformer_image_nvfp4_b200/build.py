@@ -1,4 +1,5 @@
-"""Build libklein.so (the CUDA library) in-tree with nvcc for sm_100a.
+"""Build libklein.so (the CUDA library) in-tree with nvcc for sm_100a, and
+klein_torch.so (its binding to torch tensors, for the projection path) with g++.
 
 Usage: ``python -m diffusion_transformer_image_nvfp4_b200.build [--force]``.
 """
@@ -12,6 +13,8 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libklein.so")
+BIND_PATH = os.path.join(PKG_DIR, "klein_torch.so")
+BIND_SOURCE = os.path.join(CSRC, "kl_python.cpp")
 HEADER = os.path.join(ROOT, "include", "klein.h")
 
 
@@ -23,20 +26,53 @@ def _nvcc():
 
 
 def _sources():
-    return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))] + [HEADER]
+    return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if not f.endswith(".cpp")] + [HEADER]
+
+
+def _stale(path, sources):
+    return not os.path.exists(path) or any(os.path.getmtime(s) > os.path.getmtime(path) for s in sources)
 
 
 def needs_build():
-    if not os.path.exists(LIB_PATH):
-        return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(s) > t for s in _sources())
+    return _stale(LIB_PATH, _sources())
 
 
 def build(force=False, verbose=False):
-    """Compile csrc/klein.cu into libklein.so next to this file."""
-    if not force and not needs_build():
-        return LIB_PATH
+    """Compile csrc/klein.cu into libklein.so and csrc/kl_python.cpp into
+    klein_torch.so next to this file; returns libklein.so's path."""
+    if force or needs_build():
+        _build_lib(verbose)
+    if force or _stale(BIND_PATH, [BIND_SOURCE, HEADER]):
+        _build_binding()
+    return LIB_PATH
+
+
+def _run(cmd, path):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed:\n" + r.stdout + r.stderr)
+    os.replace(path + ".tmp", path)
+    return r
+
+
+def _build_binding():
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc, cuda = os.path.join(root, "include"), os.path.dirname(os.path.dirname(_nvcc()))
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+            sysconfig.get_paths()["include"]]
+    # the system's g++ and its shared libstdc++: torch's exceptions are caught
+    # in the binding, which a C++ runtime of its own (linked statically) cannot do
+    _run([shutil.which("g++", path="/usr/bin:/usr/local/bin") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in dirs), BIND_SOURCE,
+          "-o", BIND_PATH + ".tmp", f"-L{PKG_DIR}", f"-L{os.path.join(root, 'lib')}", "-l:libklein.so", "-ltorch_python",
+          "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], BIND_PATH)
+
+
+def _build_lib(verbose):
     cmd = [
         _nvcc(),
         "-gencode", "arch=compute_100a,code=sm_100a",
@@ -48,13 +84,9 @@ def build(force=False, verbose=False):
     ]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
+    r = _run(cmd, LIB_PATH)
     if verbose:
         sys.stderr.write(r.stderr)
-    os.replace(LIB_PATH + ".tmp", LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
