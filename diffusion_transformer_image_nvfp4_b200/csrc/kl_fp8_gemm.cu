@@ -13,13 +13,13 @@
 //    TMA producer (both CTAs), scale copies + MMAs (leader), eight epilogue
 //    warps per CTA that drain the accumulator to registers, release it and
 //    store while the next tile's MMAs run.  Bound by the tensor cores.
-//  * gemm_fp8_split_kernel: few rows.  The weights take the 128-row side of
-//    the MMA and the tokens the N side (16 to 128), so one token wastes an
-//    eighth of an N = 16 instruction's columns instead of 127 of 128 rows; K
-//    is split over a cluster of up to eight CTAs so that about every SM
-//    streams a part of the weights, and the parts' fp32 sums are added in
-//    rank order through distributed shared memory: one launch, no workspace,
-//    the same bits every run.  Bound by HBM at one token.
+//  * gemm_fp8_split_kernel: few rows, or few tiles.  The weights take the
+//    128-row side of the MMA and the tokens the N side (16 to 128), so one
+//    token wastes 15 of 16 columns instead of 127 of 128 rows; where tiles are
+//    few and K is long, K is split over a cluster of up to eight CTAs so that
+//    about every SM streams a part of the weights, and the parts' fp32 sums are
+//    added in rank order through distributed shared memory: one launch, no
+//    workspace, the same bits every run.  Bound by HBM at one token.
 //
 // Either kernel can take the roles of A and W exchanged (each thread then
 // owns an output column and a warp stores 32 consecutive ones): the split
@@ -359,7 +359,6 @@ __global__ void __launch_bounds__(192, 1)
   pdl_trigger();
   const int64_t tok0 = (int64_t)xb * BT;
   const int live = (int)min((int64_t)BT, p.rows_b - tok0);  // tokens of this tile that exist
-  float v[BT];
 
   if (warp == 0) {
     int stage = 0;
@@ -409,13 +408,16 @@ __global__ void __launch_bounds__(192, 1)
         const uint32_t sfw_t = tmem + C::SF_BASE + (uint32_t)stage * C::SF_COLS;
         tmem_cp_32x128b_x4(sfw_t, desc_sf0 + soff);
         tmem_cp_32x128b_x4(sfw_t + 4, desc_sf0 + soff + 32);
+        // a column of the copied atom holds 32 of its 128 tokens: a tile of 64
+        // starts at its first or third (smaller tiles are the only one, launch_gemm_fp8)
+        const uint32_t sfx_t = sfw_t + 4 + (BT == 64 ? (uint32_t)(xb & 1) * 2u : 0u);
         const uint32_t id = idesc | idesc_scale_byte((uint32_t)kb & 3u);
         const int nk = (int)min((int64_t)4, (p.K - (int64_t)kb * 128 + 31) >> 5);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if (kk < nk)
-            mma_mxf8(tmem, desc_w0 + soff + (uint64_t)(kk * 2), desc_x0 + soff + (uint64_t)(kk * 2), id, sfw_t,
-                     sfw_t + 4, (kb > kb0 || kk > 0) ? 1u : 0u);
+            mma_mxf8(tmem, desc_w0 + soff + (uint64_t)(kk * 2), desc_x0 + soff + (uint64_t)(kk * 2), id, sfw_t, sfx_t,
+                     (kb > kb0 || kk > 0) ? 1u : 0u);
         }
         tc_commit(&empty[stage]);
       }
@@ -437,29 +439,37 @@ __global__ void __launch_bounds__(192, 1)
       tc_fence_after();
       const int quad = warp & 3;  // warps 2..5 read TMEM lanes 64.., 96.., 0.., 32..
       const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16);
-      if constexpr (BT == 128)
-        tmem_ld128(tb, v);
-      else if constexpr (BT == 64)
-        tmem_ld64(tb, v);
-      else if constexpr (BT == 32)
-        tmem_ld32(tb, v);
-      else
-        tmem_ld16(tb, v);
-      tc_fence_before();
       const int r = quad * 32 + lane;
       const int64_t n = (int64_t)wb * 128 + r;
-      if (S == 1) {
-        if (n < p.rows_a) {
+      constexpr int CH = BT < 32 ? BT : 32;
+      float* part = reinterpret_cast<float*>(smem) + r;
+      // (rolled: a launch this short is bound by fetching its instructions)
+#pragma unroll 1
+      for (int c = 0; c < BT; c += CH) {
+        float v[CH];
+        if constexpr (CH == 32)
+          tmem_ld32(tb + (uint32_t)c, v);
+        else
+          tmem_ld16(tb, v);
+        if (S > 1) {
+          // partial sums [token][128] over the stages, which nothing reads any more
 #pragma unroll
-          for (int t = 0; t < BT; ++t)
-            if (t < live) fp8_store_one(p, tok0 + t, n, v[t]);
+          for (int t = 0; t < CH; ++t) part[(c + t) * 128] = v[t];
+        } else if (n < p.rows_a) {
+          if (p.out_f32) {
+            float* o = reinterpret_cast<float*>(p.out) + (tok0 + c) * p.ldo + n;
+#pragma unroll
+            for (int t = 0; t < CH; ++t, o += p.ldo)
+              if (c + t < live) *o = v[t];
+          } else {
+            uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + (tok0 + c) * p.ldo + n;
+#pragma unroll
+            for (int t = 0; t < CH; ++t, o += p.ldo)
+              if (c + t < live) *o = (uint16_t)f32_to_bf16_bits(v[t]);
+          }
         }
-      } else {
-        // partial sums [token][128] over the stages, which nothing reads any more
-        float* part = reinterpret_cast<float*>(smem);
-#pragma unroll
-        for (int t = 0; t < BT; ++t) part[t * 128 + r] = v[t];
       }
+      tc_fence_before();
     }
   }
 
@@ -581,6 +591,86 @@ static cudaError_t launch_fp8_split(const GemmFp8Args& a, int split, cudaStream_
                             reinterpret_cast<const uint8_t*>(a.b_scales), p);
 }
 
+// Which kernel: by estimated times in us, fitted to measurements on a B200 (148
+// SMs, weights from HBM, bf16 results).  The first of the terms is what a
+// launch, or a wave of CTAs, costs without any K block; the other is the time of
+// a K block.
+//   M x N x K              measured (us)                            taken
+//   10 x 1000 x 1000       split, 16 tokens, S = 4 3.9; pair 128 5.2    split
+//   333 x 1000 x 1328      64 tokens, S = 1 5.9, 2 7.0; 128 tokens, S = 4 7.3; pair 128 9.2, 256 13.5   64, S = 1
+//   64 x 3072 x 9216       64 tokens, S = 1 21.1, 4 10.5; pair 128 20.6   64, S = 4
+//   128 x 9216 x 3072      64 tokens, S = 1 10.0; 128 tokens 10.7; pair 128 11.3   64, S = 1
+//   256 x 9216 x 3072      pair 128 11.2, 256 13.0; 128 tokens 17.0    pair 128
+//   512 x 9216 x 3072      pair 256 14.1, 128 16.8                     pair 256
+static double fp8_pair_time(const GemmFp8Args& g, int bn) {
+  const double kb = (double)((g.K + 127) / 128);
+  const int64_t tiles = (g.rows_a + 255) / 256 * ((g.rows_b + bn - 1) / bn), pairs = device_sm_count() / 2;
+  const double rounds = (double)((tiles + pairs - 1) / pairs);
+  return bn == 256 ? 6.0 + rounds * (0.30 * kb + 0.8) : 5.0 + rounds * (0.20 * kb + 0.8);
+}
+
+// CTAs that clusters of `split` fill at once (a GPC's SMs hold whole clusters only)
+template <int BT>
+static int64_t fp8_split_slots(int split) {
+  static int cache[kMaxDevices][9];
+  int dev = 0;
+  if (split == 1 || cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return device_sm_count() / split * split;
+  if (cache[dev][split] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split, 64);
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = GemmFp8SplitCfg<BT>::SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(gemm_fp8_split_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             GemmFp8SplitCfg<BT>::SMEM_BYTES) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, gemm_fp8_split_kernel<BT>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = device_sm_count() / (2 * split);  // an estimate that always fits
+    }
+    cache[dev][split] = n * split;
+  }
+  return cache[dev][split];
+}
+
+// Best tokens a tile and CTAs a cluster of the split kernel, and its time.
+static double fp8_split_plan(const GemmFp8Args& g, int64_t* bt_out, int64_t* split_out) {
+  const int64_t kb = (g.K + 127) / 128, wt = (g.rows_b + 127) / 128;
+  double best = 1e30;
+  for (int64_t bt = 16; bt <= 128; bt *= 2) {
+    const int64_t tiles = wt * ((g.rows_a + bt - 1) / bt);
+    // the scales of 16 or 32 tokens are read from the first of their 128
+    if (tiles > 65535 || (bt < 64 && g.rows_a > bt)) continue;
+    // the operands of all tiles, through L2
+    const double traffic = 2.0 + (double)tiles * (128 + bt) * g.K / 11e6;
+    for (int64_t split = 1; split <= 8 && split <= kb; ++split) {
+      if (split > 1 && tiles * split > device_sm_count()) break;
+      const int64_t slots = bt == 16   ? fp8_split_slots<16>((int)split)
+                            : bt == 32 ? fp8_split_slots<32>((int)split)
+                            : bt == 64 ? fp8_split_slots<64>((int)split)
+                                       : fp8_split_slots<128>((int)split);
+      const double waves = (double)((tiles * split + slots - 1) / slots);
+      const double blocks = (double)((kb + split - 1) / split);
+      double wave = 1.8 + 0.013 * bt + (bt == 128 ? 0.30 : 0.25) * blocks;
+      if (split > 1) wave += 1.1 + 0.03 * bt / split;
+      double t = 0.6 + waves * wave;
+      if (t < traffic) t = traffic;
+      if (t < best) {
+        best = t;
+        *bt_out = bt;
+        *split_out = split;
+      }
+    }
+    if (g.rows_a <= bt) break;
+  }
+  return best;
+}
+
 cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
   // g: A = the product's A (M rows), B = its W (N rows)
   GemmFp8Args x = g;  // roles exchanged
@@ -594,22 +684,20 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
   x.rows_b = g.rows_a;
   const int es = g.out_f32 ? 4 : 2;
   const bool rows_ok = (reinterpret_cast<uintptr_t>(g.out) & 15) == 0 && (g.ldo * es) % 16 == 0;
-  const int64_t kb = (g.K + 127) / 128;
-  const int sms = device_sm_count();
-  const int64_t bt = g.rows_a <= 16 ? 16 : g.rows_a <= 32 ? 32 : g.rows_a <= 64 ? 64 : 128;
-  const int64_t split_tiles = (g.rows_b + 127) / 128 * ((g.rows_a + bt - 1) / bt);
-  const int64_t pair_tiles = (g.rows_a + 255) / 256 * ((g.rows_b + 255) / 256);
   int kind = g.force;
-  if (kind == KL_FP8_GEMM_AUTO)
-    kind = split_tiles <= sms ? KL_FP8_GEMM_SPLIT
-           : pair_tiles >= sms / 2 ? KL_FP8_GEMM_PAIR_256x256
-                                   : KL_FP8_GEMM_PAIR_256x128;
+  int64_t bt = 0, split = 0;
+  if (kind == KL_FP8_GEMM_AUTO || kind == KL_FP8_GEMM_SPLIT) {
+    const double t = fp8_split_plan(g, &bt, &split);
+    if (kind == KL_FP8_GEMM_AUTO) {
+      const double t256 = fp8_pair_time(g, 256), t128 = fp8_pair_time(g, 128);
+      kind = t <= t256 && t <= t128 ? KL_FP8_GEMM_SPLIT
+             : t128 < t256          ? KL_FP8_GEMM_PAIR_256x128
+                                    : KL_FP8_GEMM_PAIR_256x256;
+    }
+  }
   if (kind == KL_FP8_GEMM_SPLIT) {
-    if (split_tiles > 65535) return cudaErrorInvalidValue;
-    int64_t split = sms / split_tiles;
-    split = split < 1 ? 1 : split > 8 ? 8 : split;
-    if (split > kb) split = kb;
     switch (bt) {
+      case 0: return cudaErrorInvalidValue;  // more tiles than a grid's second dimension takes
       case 16: return launch_fp8_split<16>(x, (int)split, s);
       case 32: return launch_fp8_split<32>(x, (int)split, s);
       case 64: return launch_fp8_split<64>(x, (int)split, s);

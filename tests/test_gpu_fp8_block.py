@@ -147,6 +147,16 @@ def test_product(M, N, K, kernel):
     assert kl.device_status() == "KL_OK"
 
 
+@pytest.mark.parametrize("kernel", ["auto", "split"])
+def test_product_many_token_tiles_of_few_rows(kernel):
+    # rows of very different scales: a tile that read another's scale bytes would show at once
+    for M, N, K in ((40, 128, 300), (100, 1000, 256), (200, 96, 1300), (333, 1000, 1328), (1000, 128, 640)):
+        a, w, A, W = _operands(M, N, K, M, "row")
+        got = kl.gemm_fp8_block(A, W, out_dtype=torch.float32, kernel=kernel)
+        _check_product(_np(got), _np(a), _np(w), K, False, "row")
+    assert kl.device_status() == "KL_OK"
+
+
 @pytest.mark.parametrize("split_rows", [1, 40])
 def test_product_same_bits_every_run(split_rows):
     _, _, A, W = _operands(split_rows, 384, 3000, 5)
