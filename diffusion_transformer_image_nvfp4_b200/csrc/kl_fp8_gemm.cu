@@ -52,7 +52,8 @@ struct GemmFp8Cfg {
   static constexpr int ACC = BN == 256 ? 1 : 2;
   static constexpr uint32_t SF_COLS = 16;  // A 4, W 4 * BN / 128
   static constexpr uint32_t SF_BASE = ACC * BN;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 512;
+  static constexpr int EPI_BYTES = 8 * 2048;  // a warp: 64 bytes of 32 output rows
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 512;
   static_assert(SF_BASE + STAGES * SF_COLS <= 512, "TMEM budget");
   static_assert(SMEM_BYTES <= 232448, "smem budget");
   static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
@@ -68,30 +69,43 @@ __device__ __forceinline__ void fp8_tile_at(const GemmFp8Params& p, int tile, in
   ab = g * 8 + r - bb * ga;
 }
 
-// 32 columns of one output row from n0, of which those below N exist
-__device__ __forceinline__ void fp8_store_row32(const GemmFp8Params& p, int64_t row, int64_t n0, int64_t N,
-                                                const float (&v)[32]) {
-  if (n0 >= N) return;
-  const int64_t at = row * p.ldo + n0;
-  if (n0 + 32 <= N) {  // rows are 16-byte aligned here
-    if (p.out_f32) {
-      float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
+// 64 bytes of 32 output rows from (row0, n0), a row a lane: through shared
+// memory, so that a store writes 8 rows' whole sectors instead of 16 bytes of
+// 32 rows.  16-byte unit u of row r stands at r * 64 + (u ^ (r / 2 % 4)) * 16:
+// neither side meets a bank twice.  Output rows start on 16 bytes.
+__device__ __forceinline__ void fp8_store_rows(const GemmFp8Params& p, uint8_t* buf, int lane, int64_t row0, int64_t n0,
+                                               int64_t M, int64_t N, const uint4 (&w)[4]) {
+  const int es = p.out_f32 ? 4 : 2;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) d[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    } else {
-      store_bf16x32(reinterpret_cast<uint16_t*>(p.out) + at, v);
-    }
-  } else {
+  for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(buf + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4)) = w[u];
+  __syncwarp();
+  const int unit = lane & 3;
+  const int64_t n = n0 + unit * 16 / es;
+  const int left = (int)min((int64_t)(16 / es), N - n);  // elements of the unit that exist
+  uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + n * es;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (n0 + i < N) {
-        if (p.out_f32)
-          reinterpret_cast<float*>(p.out)[at + i] = v[i];
-        else
-          reinterpret_cast<uint16_t*>(p.out)[at + i] = (uint16_t)f32_to_bf16_bits(v[i]);
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint4 q = *reinterpret_cast<const uint4*>(buf + r * 64 + ((unit ^ (r >> 1 & 3)) << 4));
+    if (row0 + r < M) {
+      uint8_t* o = out + (row0 + r) * p.ldo * es;
+      if (left * es == 16) {
+        *reinterpret_cast<uint4*>(o) = q;
+      } else if (left > 0) {
+        const uint32_t e[4] = {q.x, q.y, q.z, q.w};
+        if (p.out_f32) {
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            if (k < left) reinterpret_cast<uint32_t*>(o)[k] = e[k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 7; ++k)
+            if (k < left) reinterpret_cast<uint16_t*>(o)[k] = (uint16_t)(e[k / 2] >> (k & 1) * 16);
+        }
       }
     }
   }
+  __syncwarp();
 }
 
 __device__ __forceinline__ void fp8_store_one(const GemmFp8Params& p, int64_t m, int64_t n, float v) {
@@ -110,7 +124,8 @@ __global__ void __launch_bounds__(320, 1)
   using C = GemmFp8Cfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint8_t* epi = smem + C::STAGES * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi + C::EPI_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;  // ACC
   uint64_t* tempty = tfull + C::ACC;    // ACC (leader: 16 arrivals each)
@@ -275,17 +290,47 @@ __global__ void __launch_bounds__(320, 1)
         acc = 0;
         acc_phase ^= 1u;
       }
-      const int64_t ra = (int64_t)ab * 256 + rank * 128 + quad * 32 + lane;
+      const int64_t ra0 = (int64_t)ab * 256 + rank * 128 + quad * 32, ra = ra0 + lane;
       const int64_t rb0 = (int64_t)bb * BN + half * (BN / 2);
-      if (ra < p.rows_a) {
-        if constexpr (SWAP) {
+      if constexpr (SWAP) {
+        if (ra < p.rows_a) {
+          const int rows = (int)min((int64_t)(BN / 2), p.rows_b - rb0);  // of the output; may be negative
+          if (p.out_f32) {
+            float* o = reinterpret_cast<float*>(p.out) + rb0 * p.ldo + ra;
 #pragma unroll
-          for (int i = 0; i < BN / 2; ++i)
-            if (rb0 + i < p.rows_b) fp8_store_one(p, rb0 + i, ra, v[i]);
+            for (int i = 0; i < BN / 2; ++i, o += p.ldo)
+              if (i < rows) *o = v[i];
+          } else {
+            uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + rb0 * p.ldo + ra;
+#pragma unroll
+            for (int i = 0; i < BN / 2; ++i, o += p.ldo)
+              if (i < rows) *o = (uint16_t)f32_to_bf16_bits(v[i]);
+          }
+        }
+      } else if (ra0 < p.rows_a) {
+        uint8_t* buf = epi + (warp - 2) * 2048;
+        uint4 w[4];
+        if (p.out_f32) {
+#pragma unroll
+          for (int c = 0; c < BN / 2; c += 16) {
+            if (rb0 + c >= p.rows_b) break;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = make_uint4(__float_as_uint(v[c + 4 * u]), __float_as_uint(v[c + 4 * u + 1]),
+                                __float_as_uint(v[c + 4 * u + 2]), __float_as_uint(v[c + 4 * u + 3]));
+            fp8_store_rows(p, buf, lane, ra0, rb0 + c, p.rows_a, p.rows_b, w);
+          }
         } else {
 #pragma unroll
-          for (int c = 0; c < BN / 2; c += 32)
-            fp8_store_row32(p, ra, rb0 + c, p.rows_b, *reinterpret_cast<float(*)[32]>(v + c));
+          for (int c = 0; c < BN / 2; c += 32) {
+            if (rb0 + c >= p.rows_b) break;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = make_uint4(pack_bf16x2(v[c + 8 * u], v[c + 8 * u + 1]), pack_bf16x2(v[c + 8 * u + 2], v[c + 8 * u + 3]),
+                                pack_bf16x2(v[c + 8 * u + 4], v[c + 8 * u + 5]),
+                                pack_bf16x2(v[c + 8 * u + 6], v[c + 8 * u + 7]));
+            fp8_store_rows(p, buf, lane, ra0, rb0 + c, p.rows_a, p.rows_b, w);
+          }
         }
       }
     }
