@@ -249,14 +249,18 @@ static cudaError_t launch_rope_v(RopeParams& p, bool half, cudaStream_t s) {
   // than CTAs: one each, and parts of the heads.
   const int64_t want = (int64_t)device_sm_count() * 3;
   const int64_t most = kRopeTable / (p.pairs + 1);
-  int64_t nt = 1, least = INT64_MAX;
-  for (int64_t c = most < p.tokens ? most : p.tokens; c >= 1; --c) {
-    const int64_t n = p.batch * ((p.tokens + c - 1) / c), load = (n + want - 1) / want * c;
-    if (load < least) {
-      least = load;
+  const int64_t chunks_min = p.batch * ((p.tokens + most - 1) / most), rounds0 = (chunks_min + want - 1) / want;
+  int64_t nt = 0, least = 0;
+  for (int64_t rounds = rounds0; rounds < rounds0 + 8; ++rounds) {  // chunks of a CTA
+    int64_t chunks = rounds * want / p.batch;                       // of a batch
+    if (chunks < 1) chunks = 1;
+    const int64_t c = (p.tokens + chunks - 1) / chunks;
+    if (c <= most && (nt == 0 || rounds * c < least)) {
       nt = c;
+      least = rounds * c;
     }
   }
+  if (nt == 0) nt = most < p.tokens ? most : p.tokens;
   p.nt = (int)nt;
   p.chunks = (unsigned)((p.tokens + nt - 1) / nt);
   const int ulim = p.units < kRopeThreads ? p.units : kRopeThreads, slots = kRopeThreads / ulim;

@@ -99,6 +99,24 @@ def test_encode_nonfinite_blocks_become_nan_and_are_recorded():
     kl.device_status()
 
 
+def test_codes_past_the_last_column_are_zero_in_nan_blocks_too():
+    x = torch.full((20, 37), float("nan"), device="cuda")
+    for block, tr in (("row", False), ("row", True), ("tile", False), ("tile", True)):
+        q = kl.quantize_fp8_block(x, block, tr)
+        assert (q.codes[:, :q.cols] == 0x7F).all() and not q.codes[:, q.cols:].any()
+    assert kl.device_status() == "KL_ERR_NONFINITE"
+
+
+@pytest.mark.parametrize("off", range(0, 9))
+def test_encode_rows_at_every_alignment(off):
+    # rows start at every 16-bit and 32-bit offset within 16 bytes; the matrix ends with its buffer
+    for dtype, cols in ((torch.bfloat16, 77), (torch.float16, 530), (torch.float32, 1041)):
+        x = _x((9, cols + 3), off, dtype=dtype).cuda().flatten()[off:]
+        x = x[:(x.numel() // (cols + 2)) * (cols + 2)].view(-1, cols + 2)[:, 2:]
+        for block in ("row", "tile"):
+            _check_encode(x, kl.quantize_fp8_block(x, block), block, False)
+
+
 def test_encode_leaves_what_is_past_the_padded_columns():
     x = _x((5, 20), 6).cuda()
     codes = torch.full((5, 64), 0xAB, dtype=torch.uint8, device="cuda")

@@ -136,6 +136,19 @@ def test_staged_tiles_of_rows(R, C, groups):
     assert kl.device_status() == "KL_OK"
 
 
+@pytest.mark.parametrize("R,C,groups", [(1205, 257, 1), (2402, 1023, 2), (1501, 1025, 1), (1210, 4095, 2), (900, 2047, 3),
+                                        (700, 6143, 1), (3000, 33, 2)])
+def test_many_rows_of_odd_width(R, C, groups):
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        x, dy = _randn((R, C), 1, dtype, 2.0, 1.0), _randn((R, C + 1), 2, dtype)[:, 1:]
+        gain, bias = _params("modulate", groups, C, dtype, 3)
+        y, mean, rstd = kl.layer_norm_forward(x, gain, bias, modulate=True)
+        _check_forward(y, mean, rstd, x, gain, bias, True)
+        got = kl.layer_norm_backward(dy, x, mean, rstd, gain, modulate=True)
+        _check_backward(got, dy, x, mean, rstd, gain, True, groups)
+        assert torch.equal(kl.layer_norm_backward(dy, x, mean, rstd, gain, modulate=True, param_grads=False)[0], got[0])
+
+
 def test_strides_batches_and_alignment():
     big, dbig = _randn((30, 1000), 4, torch.bfloat16, 2.0), _randn((30, 1000), 5, torch.bfloat16)
     for cut in (lambda t: t[:, 8:520], lambda t: t[:, 3:300], lambda t: t.view(6, 5, 1000)[:, 2, :640],

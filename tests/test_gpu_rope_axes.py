@@ -77,6 +77,23 @@ def test_batches_strides_in_place_and_shared_positions():
                pairing=pairing)
 
 
+@pytest.mark.parametrize("B,T,H,dim,sections", [(1, 2000, 3, 128, (16, 24, 24)), (3, 700, 40, 64, (5, 11)), (2, 5000, 1, 8, (2, 1)),
+                                                (1, 2, 300, 128, (64,)), (5, 1, 7, 510, (255,)), (300, 3, 2, 16, (8,))])
+def test_many_tokens_heads_and_batches(B, T, H, dim, sections):
+    # several chunks a CTA, heads split over CTAs, chunks that end inside a batch
+    for dtype in (torch.bfloat16, torch.float32):
+        big = _randn((B, T, H + 1, dim + 8), 1, dtype)
+        x = big[:, :, :H, :dim]
+        pos = torch.randint(0, 500, (B, T, len(sections)), generator=torch.Generator().manual_seed(T)).int().cuda()
+        for pairing in ("interleaved", "half"):
+            y = kl.rope_axes(x, pos, sections, pairing=pairing)
+            _check(y, x, pos, sections, pairing=pairing)
+            out = torch.full_like(big, 3.0)
+            kl.rope_axes(x, pos, sections, pairing=pairing, out=out[:, :, :H, :dim])
+            assert torch.equal(out[:, :, :H, :dim], y)
+            assert (out[:, :, H:] == 3).all() and (out[..., dim:] == 3).all()
+
+
 @pytest.mark.parametrize("pt", [torch.int32, torch.int64, torch.float32])
 def test_far_positions(pt):
     # one fp64 product of a rounded frequency: 3 * 2^-53 of the angle
