@@ -514,18 +514,23 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// one vector of V elements (V * sizeof(T) = 16 bytes, or V = 1) <-> floats
+// one vector of V elements (16, 8 or 4 bytes, or V = 1) <-> floats
 template <typename T, int V>
 __device__ __forceinline__ void unpack_vec(const uint4& q, float (&v)[V]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   if constexpr (V == 8) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) unpack2<T>(w[i], v[2 * i], v[2 * i + 1]);
-  } else if constexpr (V == 4) {
+  } else if constexpr (V == 4 || V == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < V; ++i) {
+      if constexpr (sizeof(T) == 4)
+        v[i] = __uint_as_float(w[i]);
+      else if (i % 2 == 0)
+        unpack2<T>(w[i / 2], v[i], v[i + 1]);
+    }
   } else {
-    static_assert(V == 1, "vectors of 8, 4 or 1 elements");
+    static_assert(V == 1, "vectors of 8, 4, 2 or 1 elements");
     if constexpr (sizeof(T) == 4) {
       v[0] = __uint_as_float(q.x);
     } else {
@@ -539,8 +544,13 @@ __device__ __forceinline__ uint4 load_vec(const T* p) {
   if constexpr (V == 1) {
     if constexpr (sizeof(T) == 4) return make_uint4(__float_as_uint(*p), 0u, 0u, 0u);
     else return make_uint4(*reinterpret_cast<const uint16_t*>(p), 0u, 0u, 0u);
-  } else {
+  } else if constexpr (V * sizeof(T) == 16) {
     return *reinterpret_cast<const uint4*>(p);
+  } else if constexpr (V * sizeof(T) == 8) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    return make_uint4(q.x, q.y, 0u, 0u);
+  } else {
+    return make_uint4(*reinterpret_cast<const uint32_t*>(p), 0u, 0u, 0u);
   }
 }
 template <typename T, int V>
@@ -548,8 +558,14 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[V]) {
   if constexpr (V == 8) {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
-  } else if constexpr (V == 4) {
+  } else if constexpr (V == 4 && sizeof(T) == 4) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+  } else if constexpr (V == 2 && sizeof(T) == 4) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<uint32_t*>(p) = pack2<T>(v[0], v[1]);
   } else {
     *p = from_f32<T>(v[0]);
   }

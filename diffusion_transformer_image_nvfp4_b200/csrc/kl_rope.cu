@@ -28,7 +28,9 @@ namespace kl {
 
 constexpr int kRopeMaxPairs = 256;  // head dim 512
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 2;       // rows a thread loads, ahead of the two it turns and stores
+// Rows a thread loads, ahead of as many that it turns and stores (four where a
+// row is a single word: 39.7 us for 3 x 4600 x 20 heads of 100 dims, 45.5 with two).
+__host__ __device__ constexpr int rope_batch(int v, bool half) { return v == 2 && !half ? 4 : 2; }
 constexpr int kRopeTable = 2560;    // (token, pair) entries of a table buffer: two are 40 KB
 
 struct RopeParams {
@@ -124,7 +126,7 @@ struct RopeUnit {
   static __device__ __forceinline__ void entries(const float2* cs, float2 (&t)[NP]) {
     if constexpr (NP == 1) {
       t[0] = cs[0];
-    } else {  // table rows and units start on two entries
+    } else {  // table rows and units start on an even entry
 #pragma unroll
       for (int i = 0; i < NP; i += 2) {
         const float4 f = *reinterpret_cast<const float4*>(cs + i);
@@ -135,20 +137,23 @@ struct RopeUnit {
   }
   // the loaded bits themselves
   static __device__ __forceinline__ void put(T* o, const uint4& q) {
-    if constexpr (V > 1)
+    if constexpr (V * sizeof(T) == 16)
       *reinterpret_cast<uint4*>(o) = q;
-    else if constexpr (sizeof(T) == 4)
+    else if constexpr (V * sizeof(T) == 8)
+      *reinterpret_cast<uint2*>(o) = make_uint2(q.x, q.y);
+    else if constexpr (V * sizeof(T) == 4)
       *reinterpret_cast<uint32_t*>(o) = q.x;
     else
       *reinterpret_cast<uint16_t*>(o) = (uint16_t)q.x;
   }
 };
 
-// V elements a thread at a time (16 bytes, or V = 1 for what is not aligned;
-// interleaved pairs then move two elements).  A thread keeps one unit u of the
+// V elements a thread at a time (16 bytes, two elements, or V = 1 for what is
+// not aligned; interleaved pairs then move two elements).  A thread keeps one unit u of the
 // head and walks the rows.
 template <typename T, int V, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_axes_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kRopeBatch = rope_batch(V, HALF);
   extern __shared__ __align__(16) float2 rope_tables[];  // [2][nt][pairs, even] (cos, sin)
   pdl_wait();
   pdl_trigger();
@@ -281,10 +286,16 @@ template <typename T>
 static cudaError_t launch_rope(RopeParams& p, bool half, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const int64_t str[6] = {p.xs_b, p.xs_t, p.xs_h, p.os_b, p.os_t, p.os_h};
-  bool vec = ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out)) & 15) == 0 && p.dim % V == 0;
-  for (int64_t st : str) vec = vec && st % V == 0;
-  if (half) vec = vec && p.pairs % V == 0;
-  return vec ? launch_rope_v<T, V>(p, half, s) : launch_rope_v<T, 1>(p, half, s);
+  auto fits = [&](int v) {  // every vector of v dims lies on its own size
+    bool ok = ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out)) % (v * sizeof(T))) == 0 &&
+              p.dim % v == 0 && (!half || p.pairs % v == 0);
+    for (int64_t st : str) ok = ok && st % v == 0;
+    return ok;
+  };
+  // 3 x 4600 x 20 heads of 100 dims, bf16, interleaved and half: 39.7 and 36.3 us with
+  // two elements, 47.7 and 58.4 with one
+  if (fits(V)) return launch_rope_v<T, V>(p, half, s);
+  return fits(2) ? launch_rope_v<T, 2>(p, half, s) : launch_rope_v<T, 1>(p, half, s);
 }
 
 }  // namespace kl
