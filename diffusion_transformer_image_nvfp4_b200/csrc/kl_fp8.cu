@@ -156,9 +156,8 @@ struct Fp8EncodeParams {
 };
 
 // Row blocks.  A warp takes up to `seg` words (a word: the four blocks of 512
-// columns) of one row, the next word's loads ahead of this one's work; with
-// the MMA layout also the padding rows up to a multiple of 128, whose words it
-// zeroes.
+// columns) of one row; with the MMA layout also the padding rows up to a
+// multiple of 128, whose words it zeroes.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) fp8_encode_rows_kernel(const Fp8EncodeParams p, int64_t tasks, uint64_t rcp_nseg,
                                                               int nseg, int seg, int words) {
@@ -184,19 +183,42 @@ __global__ void __launch_bounds__(256) fp8_encode_rows_kernel(const Fp8EncodePar
     }
     const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx + c;
     uint8_t* out = p.codes + row * p.ldc + c;
-    Fp8Raw<T> next;
-    next.template load<VEC>(x, cols - c, lo, hi);
-    for (int k = k0; k < k1; ++k) {
-      const Fp8Raw<T> raw = next;
-      const int n = cols - c;
-      x += 512;
-      c += 512;
-      if (k + 1 < k1) next.template load<VEC>(x, cols - c, lo, hi);
+    const int sstep = p.mma ? 512 : 4;
+    // scale byte of a lane's block from its part of the block's amax
+    auto scale = [&](const Fp8Raw<T>& raw) {
       uint32_t m = raw.amax_bits();
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       const uint32_t byte = fp8_scale_byte(m);
       bad |= byte == 255u;
+      return byte;
+    };
+    int k = k0;
+    if (VEC) {  // words without an end, two at a time
+      const int kf = min(k1, cols >> 9);
+      for (; k + 1 < kf; k += 2) {
+        Fp8Raw<T> raw[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) raw[i].template load<true>(x + i * 512, 16, lo, hi);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t byte = scale(raw[i]);
+          float v[16];
+          raw[i].values(v);
+          *reinterpret_cast<uint4*>(out + i * 512) = fp8_codes16(v, fp8_inv2(byte), 16);
+          if ((lane & 7) == 0) sc[i * sstep] = (uint8_t)byte;
+        }
+        x += 1024;
+        out += 1024;
+        sc += 2 * sstep;
+        c += 1024;
+      }
+    }
+    for (; k < k1; ++k) {
+      const int n = cols - c;
+      Fp8Raw<T> raw;
+      raw.template load<VEC>(x, n, lo, hi);
+      const uint32_t byte = scale(raw);
       float v[16];
       raw.values(v);
       if (n > 0) *reinterpret_cast<uint4*>(out) = fp8_codes16(v, fp8_inv2(byte), n);
@@ -206,8 +228,10 @@ __global__ void __launch_bounds__(256) fp8_encode_rows_kernel(const Fp8EncodePar
         else if (p.mma)
           *sc = 0;
       }
+      x += 512;
       out += 512;
-      sc += p.mma ? 512 : 4;
+      sc += sstep;
+      c += 512;
     }
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(KL_DEVERR_NONFINITE);
