@@ -246,9 +246,10 @@ __global__ void __launch_bounds__(8 * PAIRS) fp8_encode_columns_kernel(const Fp8
   __shared__ uint32_t colmax[TILE ? 1 : 8][2 * PAIRS];
   pdl_wait();
   pdl_trigger();
-  // a warp: 8 pairs of 64 rows, so both its reads and its writes are whole sectors
-  constexpr int WP = PAIRS / 8;
-  const int tid = threadIdx.x, pair = (tid & 7) + tid / 32 % WP * 8, q = (tid >> 3 & 3) + tid / (32 * WP) * 4;
+  // a warp: LP pairs of 16 * 32 / LP rows, so both its reads and its writes are whole sectors
+  constexpr int LP = sizeof(T) == 2 ? 16 : 8, WP = PAIRS / LP;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int pair = lane % LP + tid / 32 % WP * LP, q = lane / LP + tid / (32 * WP) * (32 / LP);
   const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
   const int64_t r0 = tr * 128 + q * 16, c0 = tc * (2 * PAIRS) + 2 * pair;
   const int nr = (int)max((int64_t)0, min((int64_t)16, p.rows - r0));
