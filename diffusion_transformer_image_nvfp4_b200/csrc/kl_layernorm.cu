@@ -48,6 +48,8 @@ struct LnParams {
   float eps;
   float* part;  // backward: [groups][splits][2][cols] partial sums (null: none wanted)
   int splits;   // CTAs of a group
+  float* dgain; // backward of few rows
+  float* dbias;
 };
 
 // V parameter values of type KIND at an address aligned for a load of V (V = 1: any)
@@ -415,11 +417,8 @@ __global__ void __launch_bounds__(1024) ln_forward_wide_kernel(const LnParams p)
 // splits * blockDim.y.  The next row's x and dy are loaded before this row's
 // sums are waited for.
 template <typename T, int V, int NV, bool PG>
-__global__ void __launch_bounds__(512, NV == 1 || V == 1 ? 2 : 1)
-    ln_backward_kernel(const LnParams p) {
+__device__ __forceinline__ void ln_backward_rows(const LnParams& p) {
   extern __shared__ float ln_red[];  // [2][blockDim.y][32][2]; then [blockDim.y][2][cols padded] if PG and blockDim.y > 1
-  pdl_wait();
-  pdl_trigger();
   const int64_t group = blockIdx.x / p.splits, split = blockIdx.x - group * p.splits;
   const int64_t r0 = group * p.group_rows;
   const int64_t step = (int64_t)p.splits * blockDim.y;
@@ -538,6 +537,51 @@ __global__ void __launch_bounds__(512, NV == 1 || V == 1 ? 2 : 1)
         }
       }
     }
+  }
+}
+template <typename T, int V, int NV, bool PG>
+__global__ void __launch_bounds__(512, NV == 1 || V == 1 ? 2 : 1) ln_backward_kernel(const LnParams p) {
+  pdl_wait();
+  pdl_trigger();
+  ln_backward_rows<T, V, NV, PG>(p);
+}
+
+// Few rows: one launch.  The first row_ctas CTAs are the kernel above without
+// the parameters' sums; the others take 32 columns of a group each and add
+// those columns over the group's rows, warps taking rows in turn, from x and
+// dy as the caches hold them.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512, NV == 1 || V == 1 ? 2 : 1)
+    ln_backward_few_kernel(const LnParams p, unsigned row_ctas) {
+  __shared__ float red[2][16][33];
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x < row_ctas) {
+    ln_backward_rows<T, V, NV, false>(p);
+    return;
+  }
+  const unsigned blocks = (unsigned)((p.cols + 31) / 32), at = blockIdx.x - row_ctas, group = at / blocks;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int nw = (blockDim.x * blockDim.y) >> 5, rows = (int)p.group_rows;
+  const int64_t c = (int64_t)(at - group * blocks) * 32 + lane, r0 = group * p.group_rows;
+  float g = 0.f, b = 0.f;
+  if (c < p.cols) {
+    const T* x = reinterpret_cast<const T*>(p.x) + r0 * p.ldx + c;
+    const T* dy = reinterpret_cast<const T*>(p.dy) + r0 * p.ldy + c;
+#pragma unroll 8
+    for (int r = w; r < rows; r += nw) {
+      const float d = to_f32(dy[r * p.ldy]);
+      g = fmaf(d, (to_f32(x[r * p.ldx]) - p.mean[r0 + r]) * p.rstd[r0 + r], g);
+      b += d;
+    }
+  }
+  red[0][w][lane] = g;
+  red[1][w][lane] = b;
+  __syncthreads();
+  if (w < 2 && c < p.cols) {
+    float s = red[w][0][lane];
+    for (int i = 1; i < nw; ++i) s += red[w][i][lane];
+    (w == 0 ? p.dgain : p.dbias)[group * p.cols + c] = s;
   }
 }
 
@@ -990,6 +1034,8 @@ __global__ void __launch_bounds__(512) ln_param_sum_kernel(const float* __restri
 // and a CTA takes one (as for groups of a few rows, whose parameters would be
 // staged for nothing).
 constexpr int64_t kLnWarpRows = 4 * kNumSMs;
+// up to these rows of a group, and bytes of x, the backward is one launch
+constexpr int64_t kLnFewRows = 400, kLnFewBytes = 8 << 20;
 
 // How a row is spread over threads: vectors of V elements where every row
 // starts on 16 bytes, else single elements; nv vectors a thread (0: too wide
@@ -1127,11 +1173,24 @@ static cudaError_t launch_ln_forward(LnParams& p, bool vec, cudaStream_t s) {
 template <typename T, int V, int NV>
 static cudaError_t launch_ln_backward_nv(const LnParams& p, const LnShape& sh, cudaStream_t s) {
   size_t smem = (size_t)sh.ty * 128 * sizeof(float);
+  if (p.dgain && !p.part) {
+    const int64_t groups = p.rows / p.group_rows, row_ctas = groups * p.splits;
+    return launch_pdl(ln_backward_few_kernel<T, V, NV>, dim3((unsigned)(row_ctas + groups * ((p.cols + 31) / 32))),
+                      dim3(sh.tx, sh.ty), smem, s, p, (unsigned)row_ctas);
+  }
   if (p.part && sh.ty > 1) smem += (size_t)sh.ty * 2 * NV * V * sh.tx * sizeof(float);
   const dim3 grid((unsigned)(p.rows / p.group_rows * p.splits)), block(sh.tx, sh.ty);
   return p.part ? launch_pdl(ln_backward_kernel<T, V, NV, true>, grid, block, smem, s, p)
                 : launch_pdl(ln_backward_kernel<T, V, NV, false>, grid, block, smem, s, p);
 }
+// One launch for the rows and the parameters' sums where a second launch (3 us
+// of the GPU, as much of the CPU) costs more than reading x and dy twice.
+// One and two launches, us: 77 x 1155 fp32 2.9 and 5.2, 300 x 3072 bf16 5.1 and
+// 7.9, 450 x 3072 8.7 and 8.8, 1000 x 1024 10.2 and 9.5.
+static bool ln_few(int64_t groups, int64_t group_rows, int64_t cols, int es, bool vec) {
+  return group_rows <= kLnFewRows && groups * group_rows * cols * es <= kLnFewBytes && ln_shape(cols, es, vec, true).nv > 0;
+}
+
 template <typename T, int NV, bool PG, bool TEAMS>
 static cudaError_t launch_ln_tile(const LnParams& p, const LnTile& t, cudaStream_t s) {
   const size_t smem = (size_t)t.teams * t.stages * 2 * kLnTileRows * p.cols * sizeof(T);
@@ -1160,7 +1219,8 @@ template <typename T>
 static cudaError_t launch_ln_backward(LnParams& p, bool vec, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const LnTile t = ln_tile(p.rows / p.group_rows, p.group_rows, p.cols, sizeof(T), vec);
-  if (t.ok) return p.part ? launch_ln_tiles<T, true>(p, t, vec, s) : launch_ln_tiles<T, false>(p, t, vec, s);
+  if (t.ok && !ln_few(p.rows / p.group_rows, p.group_rows, p.cols, sizeof(T), vec))
+    return p.part ? launch_ln_tiles<T, true>(p, t, vec, s) : launch_ln_tiles<T, false>(p, t, vec, s);
   const LnShape sh = ln_shape(p.cols, sizeof(T), vec, true);
   if (sh.nv == 0) {
     cudaError_t e = launch_pdl(ln_backward_wide_kernel<T>, dim3((unsigned)p.rows), dim3(1024), 256, s, p);
@@ -1241,6 +1301,7 @@ size_t kl_layer_norm_backward_workspace_size(int dtype, int64_t rows, int64_t co
   int most = 0;
   const int es = ln_es(dtype), layouts = cols % (16 / es) == 0 ? 2 : 1;
   for (int vec = 0; vec < layouts; ++vec) {
+    if (ln_few(groups, rows / groups, cols, es, vec != 0)) continue;
     const LnTile t = ln_tile(groups, rows / groups, cols, es, vec != 0);
     const int s = t.ok ? t.splits : ln_splits(groups, rows / groups, ln_shape(cols, es, vec != 0, true));
     most = s > most ? s : most;
@@ -1262,9 +1323,9 @@ kl_status kl_layer_norm_backward(const void* dy, int64_t lddy, const void* x, in
       !aligned(rstd, 4) || (dgain && (!aligned(dgain, 4) || !aligned(dbias, 4))))
     return KL_ERR_MISALIGNED;
   if (dgain) {
-    if (!workspace || ws_bytes < kl_layer_norm_backward_workspace_size(dtype, rows, cols, groups))
-      return KL_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return KL_ERR_MISALIGNED;
+    const size_t need = kl_layer_norm_backward_workspace_size(dtype, rows, cols, groups);
+    if (need && (!workspace || ws_bytes < need)) return KL_ERR_WORKSPACE;
+    if (need && !aligned(workspace, 16)) return KL_ERR_MISALIGNED;
   }
   if ((st = check_arch()) != KL_OK) return st;
   LnParams p{};
@@ -1282,16 +1343,19 @@ kl_status kl_layer_norm_backward(const void* dy, int64_t lddy, const void* x, in
   p.group_rows = rows / groups;
   p.mean = const_cast<float*>(mean);
   p.rstd = const_cast<float*>(rstd);
-  p.part = dgain ? reinterpret_cast<float*>(workspace) : nullptr;
   const bool vec = cols % (16 / es) == 0 && ln_rows_16(x, ldx, es) && ln_rows_16(dy, lddy, es) && ln_rows_16(dx, lddx, es) &&
                    ln_param_vec(gain, es, ps);
+  const bool few = ln_few(groups, p.group_rows, cols, es, vec);
+  p.part = dgain && !few ? reinterpret_cast<float*>(workspace) : nullptr;
+  p.dgain = dgain;
+  p.dbias = dbias;
   const LnTile tile = ln_tile(groups, p.group_rows, cols, es, vec);
-  p.splits = tile.ok ? tile.splits : ln_splits(groups, p.group_rows, ln_shape(cols, es, vec, true));
+  p.splits = tile.ok && !few ? tile.splits : ln_splits(groups, p.group_rows, ln_shape(cols, es, vec, true));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = dtype == KL_BF16  ? launch_ln_backward<__nv_bfloat16>(p, vec, s)
                   : dtype == KL_F16 ? launch_ln_backward<__half>(p, vec, s)
                                     : launch_ln_backward<float>(p, vec, s);
-  if (e == cudaSuccess && dgain)
+  if (e == cudaSuccess && p.part)
     e = launch_pdl(ln_param_sum_kernel, dim3((unsigned)((2 * cols + 31) / 32), (unsigned)groups), dim3(32, 16), 0, s,
                    (const float*)p.part, p.splits, cols, dgain, dbias);
   return e == cudaSuccess ? KL_OK : cuda_fail(e);

@@ -334,7 +334,7 @@ if (truth(a[7])) {
   dgain = empty({p.groups, r.cols}, at::kFloat, dev);
   dbias = empty({p.groups, r.cols}, at::kFloat, dev);
   bytes = kl_layer_norm_backward_workspace_size(dtype, r.rows, r.cols, p.groups);
-  ws = empty({(int64_t)bytes}, at::kByte, dev);
+  if (bytes) ws = empty({(int64_t)bytes}, at::kByte, dev);
 }
 call(dev, "kl_layer_norm_backward", [&](void* s) {
   return kl_layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), r.ld, dtype, r.rows, r.cols,

@@ -28,9 +28,8 @@ namespace kl {
 
 constexpr int kRopeMaxPairs = 256;  // head dim 512
 constexpr int kRopeThreads = 256;
-// Rows a thread loads, ahead of as many that it turns and stores (four where a
-// row is a single word: 39.7 us for 3 x 4600 x 20 heads of 100 dims, 45.5 with two).
-__host__ __device__ constexpr int rope_batch(int v, bool half) { return v == 2 && !half ? 4 : 2; }
+// rows a thread loads, ahead of as many that it turns and stores
+__host__ __device__ constexpr int rope_batch(int bytes, bool half) { return half && bytes >= 16 ? 2 : 4; }
 constexpr int kRopeTable = 2560;    // (token, pair) entries of a table buffer: two are 40 KB
 
 struct RopeParams {
@@ -77,14 +76,12 @@ struct RopeUnit {
       a = load_vec<T, V>(x + u * V);
     }
   }
-  // cs: the table's row from the unit's first pair; whole: all its dims turn
+  // whole: all its dims turn, by t; else cs is the table's row from the unit's first pair
   __device__ __forceinline__ void store(T* o, const RopeParams& p, int u, int pair_units, bool whole,
-                                        const float2* cs) {
+                                        const float2 (&t)[NP], const float2* cs) {
     if constexpr (HALF || V == 1) {
       if (whole) {
         float va[V], vc[V];
-        float2 t[V];
-        entries(cs, t);
         unpack_vec<T, V>(a, va);
         unpack_vec<T, V>(c, vc);
 #pragma unroll
@@ -106,8 +103,6 @@ struct RopeUnit {
       float v[V];
       unpack_vec<T, V>(a, v);
       if (whole) {
-        float2 t[NP];
-        entries(cs, t);
 #pragma unroll
         for (int i = 0; i < NP; ++i) turn(v[2 * i], v[2 * i + 1], t[i]);
       } else {
@@ -151,9 +146,14 @@ struct RopeUnit {
 // V elements a thread at a time (16 bytes, two elements, or V = 1 for what is
 // not aligned; interleaved pairs then move two elements).  A thread keeps one unit u of the
 // head and walks the rows.
-template <typename T, int V, bool HALF>
+// HEADS: a token's heads are more than the slots, so a thread's rows of a token
+// are `slots` heads apart and share its table entries; else several tokens'
+// heads are spread over the slots, and a thread's rows are one head of tokens
+// `tpar` apart.  Either way a batch of rows lies at one stride.
+template <typename T, int V, bool HALF, bool HEADS>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_axes_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int kRopeBatch = rope_batch(V, HALF);
+  constexpr int B = rope_batch(V * (int)sizeof(T), HALF);
+  using Unit = RopeUnit<T, V, HALF>;
   extern __shared__ __align__(16) float2 rope_tables[];  // [2][nt][pairs, even] (cos, sin)
   pdl_wait();
   pdl_trigger();
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_axes_kernel(const __grid
   while (tj >= p.first[axis + 1]) ++axis;
   const int ulim = min(p.units, kRopeThreads), slots = kRopeThreads / ulim;
   const int u0 = tid % ulim, slot = tid / ulim;
-  const int pair_units = p.pairs / RopeUnit<T, V, HALF>::NP, pitch = (p.pairs + 1) & ~1;
+  const int pair_units = p.pairs / Unit::NP, pitch = (p.pairs + 1) & ~1;
   int buf = 0;
   for (unsigned item = blockIdx.x; item < p.items; item += gridDim.x, buf ^= 1) {
     const unsigned bc = p.hparts == 1 ? item : item / (unsigned)p.hparts, b = p.batch == 1 ? 0u : bc / p.chunks;
@@ -173,39 +173,49 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_axes_kernel(const __grid
     const int h0 = (int)(item - bc * p.hparts) * p.hper, nh = min(p.hper, p.heads - h0);
     const int nt = (int)min((int64_t)p.nt, p.tokens - t0);
     float2* table = rope_tables + buf * p.nt * pitch;
-    // the thread's rows are `slots` apart: a step of dt tokens and dh heads,
-    // and one of a token back by a turn of the heads where that passes the last
-    const int rows = slot < slots ? nt * nh : 0, dt = slots / nh, dh = slots - dt * nh, ts0 = slot / nh;
-    const int64_t xstep = dt * p.xs_t + dh * p.xs_h, xturn = p.xs_t - nh * p.xs_h;
-    const int64_t ostep = dt * p.os_t + dh * p.os_h, oturn = p.os_t - nh * p.os_h;
-    const int cstep = dt * pitch;
-    int u = u0, h = slot - ts0 * nh, r = slot;
-    const T* x = reinterpret_cast<const T*>(p.x) + b * p.xs_b + (t0 + ts0) * p.xs_t + (h0 + h) * p.xs_h;
-    T* o = reinterpret_cast<T*>(p.out) + b * p.os_b + (t0 + ts0) * p.os_t + (h0 + h) * p.os_h;
-    const float2* cs = table + ts0 * pitch;
-    RopeUnit<T, V, HALF> next[kRopeBatch];
-    T* nout[kRopeBatch];
-    const float2* ncs[kRopeBatch];
-    auto fetch = [&] {  // the next rows' loads (those past the last are not made)
+    const int tpar = HEADS ? 1 : slots / nh;  // tokens side by side
+    const int h = HEADS ? slot : slot % nh, tp = HEADS ? 0 : slot / nh;
+    const bool live = slot < slots && tp < tpar;
+    // rows of a run (a token's heads, or all tokens), and what one is from the next
+    const int run = !live ? 0 : HEADS ? (nh - h + slots - 1) / slots : (nt - tp + tpar - 1) / tpar;
+    const int64_t xk = HEADS ? slots * p.xs_h : tpar * p.xs_t, ok = HEADS ? slots * p.os_h : tpar * p.os_t;
+    const int ck = HEADS ? 0 : tpar * pitch;
+    const T* x0 = reinterpret_cast<const T*>(p.x) + b * p.xs_b + (t0 + tp) * p.xs_t + (h0 + h) * p.xs_h;
+    T* o0 = reinterpret_cast<T*>(p.out) + b * p.os_b + (t0 + tp) * p.os_t + (h0 + h) * p.os_h;
+    struct Batch {
+      const T* x;
+      T* o;
+      const float2* cs;
+      int left, t;  // rows left in the run, the run
+    } next;
+    const int runs = HEADS ? nt : 1;
+    Unit qn[B];
+    int u = u0;
+    auto start = [&] { next = Batch{x0, o0, table + tp * pitch + u * Unit::NP, run, run > 0 ? 0 : runs}; };
+    auto fetch = [&] {
+      const T* x = next.x;
 #pragma unroll
-      for (int k = 0; k < kRopeBatch; ++k) {
-        nout[k] = o;
-        ncs[k] = cs;
-        if (r < rows) next[k].load(x, p, u, pair_units);
-        r += slots;
-        x += xstep;
-        o += ostep;
-        cs += cstep;
-        h += dh;
-        if (h >= nh) {
-          h -= nh;
-          x += xturn;
-          o += oturn;
-          cs += pitch;
+      for (int k = 0; k < B; ++k, x += xk)
+        if (k < next.left) qn[k].load(x, p, u, pair_units);
+    };
+    auto advance = [&] {
+      next.left -= B;
+      if (next.left > 0) {
+        next.x += B * xk;
+        next.o += B * ok;
+        next.cs += B * ck;
+      } else {
+        ++next.t;
+        if constexpr (HEADS) {
+          next.left = run;
+          next.x = x0 + next.t * p.xs_t;
+          next.o = o0 + next.t * p.os_t;
+          next.cs += pitch;
         }
       }
     };
-    fetch();  // under way while the table is made
+    start();
+    if (next.t < runs) fetch();  // under way while the table is made
     if (ts < tslots) {
       for (int t = ts; t < nt; t += tslots) {
         const double a = rope_pos(p, (b * p.pos_b + t0 + t) * p.naxes + axis) * freq;
@@ -216,32 +226,33 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_axes_kernel(const __grid
     }
     __syncthreads();
     while (true) {
-      for (int done = slot; done < rows; done += kRopeBatch * slots) {
-        RopeUnit<T, V, HALF> q[kRopeBatch];
-        T* out[kRopeBatch];
-        const float2* row[kRopeBatch];
+      const bool whole = u < pair_units;
+#pragma unroll 2
+      while (next.t < runs) {
+        Unit q[B];
 #pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k) {
-          q[k] = next[k];
-          out[k] = nout[k];
-          row[k] = ncs[k];
-        }
+        for (int k = 0; k < B; ++k) q[k] = qn[k];
+        const Batch cur = next;
         // x and out may be the same tensor: the compiler cannot move these
         // loads above the stores itself
-        fetch();
+        advance();
+        if (next.t < runs) fetch();
+        float2 e[Unit::NP];
+        if (HEADS && whole) Unit::entries(cur.cs, e);
+        T* o = cur.o;
+        const float2* cs = cur.cs;
 #pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k)
-          if (done + k * slots < rows)
-            q[k].store(out[k], p, u, pair_units, u < pair_units, row[k] + u * RopeUnit<T, V, HALF>::NP);
+        for (int k = 0; k < B; ++k, o += ok, cs += ck) {
+          if (k < cur.left) {
+            if (!HEADS && whole) Unit::entries(cs, e);
+            q[k].store(o, p, u, pair_units, whole, e, cs);
+          }
+        }
       }
       if ((u += kRopeThreads) >= p.units) break;
       // (heads of more than 256 units, which single elements can have: again from the first row)
-      h = slot - ts0 * nh;
-      r = slot;
-      x = reinterpret_cast<const T*>(p.x) + b * p.xs_b + (t0 + ts0) * p.xs_t + (h0 + h) * p.xs_h;
-      o = reinterpret_cast<T*>(p.out) + b * p.os_b + (t0 + ts0) * p.os_t + (h0 + h) * p.os_h;
-      cs = table + ts0 * pitch;
-      fetch();
+      start();
+      if (next.t < runs) fetch();
     }
   }
 }
@@ -278,8 +289,9 @@ static cudaError_t launch_rope_v(RopeParams& p, bool half, cudaStream_t s) {
   p.items = (unsigned)(p.batch * p.chunks * p.hparts);
   const unsigned grid = p.items < (unsigned)want ? p.items : (unsigned)want;
   const size_t smem = (size_t)2 * nt * ((p.pairs + 1) & ~1) * sizeof(float2);
-  return half ? launch_pdl(rope_axes_kernel<T, V, true>, dim3(grid), dim3(kRopeThreads), smem, s, p)
-              : launch_pdl(rope_axes_kernel<T, V, false>, dim3(grid), dim3(kRopeThreads), smem, s, p);
+  auto kern = p.hper >= slots ? (half ? rope_axes_kernel<T, V, true, true> : rope_axes_kernel<T, V, false, true>)
+                              : (half ? rope_axes_kernel<T, V, true, false> : rope_axes_kernel<T, V, false, false>);
+  return launch_pdl(kern, dim3(grid), dim3(kRopeThreads), smem, s, p);
 }
 
 template <typename T>
@@ -292,8 +304,8 @@ static cudaError_t launch_rope(RopeParams& p, bool half, cudaStream_t s) {
     for (int64_t st : str) ok = ok && st % v == 0;
     return ok;
   };
-  // 3 x 4600 x 20 heads of 100 dims, bf16, interleaved and half: 39.7 and 36.3 us with
-  // two elements, 47.7 and 58.4 with one
+  // 3 x 4600 x 20 heads of 100 dims, bf16, in place of single elements: 32.7 us for
+  // 47.7 interleaved, 35.8 for 57.4 half
   if (fits(V)) return launch_rope_v<T, V>(p, half, s);
   return fits(2) ? launch_rope_v<T, 2>(p, half, s) : launch_rope_v<T, 1>(p, half, s);
 }

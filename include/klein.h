@@ -739,7 +739,8 @@ kl_status kl_rope_axes(const kl_rope_args* args, void* stream);
  *   dgain[group, c] = sum of dy * xhat, dbias = sum of dy over the group's
  *   rows, fp32 [groups, cols], both or neither (NULL: dx alone, no workspace).
  * The sums are taken in a fixed order.  Outputs must not overlap inputs.
- * workspace: >= kl_layer_norm_backward_workspace_size bytes, 16-byte aligned.
+ * workspace: >= kl_layer_norm_backward_workspace_size bytes, 16-byte aligned
+ *   (0 bytes, and NULL, for few rows: those take one launch).
  */
 #define KL_LN_MODULATE 1
 #define KL_LN_MAX_ROWS 0x7FFFFFFF

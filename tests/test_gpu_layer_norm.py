@@ -149,6 +149,19 @@ def test_many_rows_of_odd_width(R, C, groups):
         assert torch.equal(kl.layer_norm_backward(dy, x, mean, rstd, gain, modulate=True, param_grads=False)[0], got[0])
 
 
+@pytest.mark.parametrize("R,C,groups", [(400, 64, 1), (401, 64, 1), (399, 3072, 1), (800, 1155, 2), (1600, 2048, 4),
+                                        (1024, 1024, 512), (2, 40, 2)])
+def test_one_and_two_launches(R, C, groups):
+    # on both sides of where the parameters' sums take a launch of their own
+    for dtype in (torch.bfloat16, torch.float32):
+        x, dy = _randn((R, C), 1, dtype, 2.0, 1.0), _randn((R, C), 2, dtype)
+        gain, bias = _params("gain", groups, C, dtype, 3)
+        _, mean, rstd = kl.layer_norm_forward(x, gain, bias)
+        got = kl.layer_norm_backward(dy, x, mean, rstd, gain)
+        _check_backward(got, dy, x, mean, rstd, gain, False, groups)
+        assert all(torch.equal(a, b) for a, b in zip(got, kl.layer_norm_backward(dy, x, mean, rstd, gain)))
+
+
 def test_strides_batches_and_alignment():
     big, dbig = _randn((30, 1000), 4, torch.bfloat16, 2.0), _randn((30, 1000), 5, torch.bfloat16)
     for cut in (lambda t: t[:, 8:520], lambda t: t[:, 3:300], lambda t: t.view(6, 5, 1000)[:, 2, :640],
