@@ -337,6 +337,11 @@ extern "C" kl_status kl_rope_axes(const kl_rope_args* r, void* stream) {
   const int es = r->dtype == KL_F32 ? 4 : 2;
   if (!aligned(r->x, es) || !aligned(r->out, es) || !aligned(r->pos, r->pos_type == KL_POS_I64 ? 8 : 4))
     return KL_ERR_MISALIGNED;
+  // no output element twice; in place only element by element
+  const int64_t size[3] = {r->batch, r->tokens, r->heads};
+  for (int i = 0; i < 3; ++i)
+    if (size[i] > 1 && (r->out_stride[i] == 0 || (r->x == r->out && r->x_stride[i] != r->out_stride[i])))
+      return KL_ERR_INVALID_ARG;
   kl_status st = check_arch();
   if (st != KL_OK) return st;
   p.x = r->x;

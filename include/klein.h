@@ -622,8 +622,10 @@ kl_status kl_dit_step_cached(const kl_dit_shape* shape, const kl_dit_weights* w,
  * an FP8 encode and product, rotary positions applied to a tensor, and
  * LayerNorm with its backward pass.  Rows have strides (ld, in elements), any
  * number of columns, and bf16, fp16 or fp32 elements; pointers need only the
- * alignment of their element type unless stated.  None of these calls uses
- * a workspace except kl_layer_norm_backward; none keeps anything between calls.
+ * alignment of their element type unless stated.  Every size is at least 1
+ * (KL_ERR_UNSUPPORTED_SHAPE otherwise).  None of these calls uses a workspace
+ * except kl_layer_norm_backward; none keeps anything between calls.  All of
+ * them may be captured into a CUDA graph, the first call of a process included.
  * ---------------------------------------------------------------------- */
 #define KL_BF16 0
 #define KL_F32 1

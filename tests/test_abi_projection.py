@@ -75,6 +75,12 @@ def test_rope_refusals(L):
     assert r(sections=(16, 24, 25, 0)) == r(sections=(0, 0, 0, 0)) == r(sections=(-1, 24, 24, 0)) == SHAPE
     assert r(dim=514) == r(dim=127) == r(tokens=0) == r(heads=0) == r(batch=0) == SHAPE
     assert r(batch=1 << 20, tokens=1 << 20) == SHAPE
+    def st(*v):
+        return (ctypes.c_int64 * 3)(*v)
+
+    # (x is out here) in place at other strides; an output that is broadcast
+    assert r(out_stride=st(0, 256, 127)) == r(x_stride=st(0, 0, 128)) == INVALID
+    assert r(out=2 * FAKE, out_stride=st(0, 0, 128)) == r(out=2 * FAKE, batch=2, out_stride=st(0, 256, 128)) == INVALID
     assert r(x=FAKE + 1) == r(out=FAKE + 1) == r(pos=FAKE + 2) == r(pos=FAKE + 4, pos_type=1) == MISALIGNED
 
 

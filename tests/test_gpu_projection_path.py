@@ -2,6 +2,10 @@
 modulation, encode, QKV product, rotary positions on q and k in place, joint
 attention; and the same layer's backward pass up to the attention."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -136,3 +140,35 @@ def test_backward(T, H):
     # bf16 dx: each term off by 2^-8 of itself; the saved statistics are fp32
     assert abs(diff - (_np(dx) * u).sum()) <= (np.abs(_np(dx) * u) * 2.0 ** -8).sum() + 1e-4 * np.abs(rx * u).sum()
     assert kl.device_status() == "KL_OK"
+
+
+def test_first_calls_of_a_process_captured():
+    # nothing is loaded, queried or set up in a way that a capture forbids
+    code = """
+import torch, diffusion_transformer_image_nvfp4_b200 as kl
+def captured(f):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = f()
+    g.replay()
+    torch.cuda.synchronize()
+    return r
+def same(a, b):
+    assert all(torch.equal(i, j) for i, j in zip(a, b))
+x, w = (torch.randn(n, 1328, device="cuda").bfloat16() for n in (3000, 1000))
+W = captured(lambda: kl.quantize_fp8_block(w, "tile"))
+for rows in (1, 333, 3000):
+    A = captured(lambda: kl.quantize_fp8_block(x[:rows]))
+    same([captured(lambda: kl.gemm_fp8_block(A, W))], [kl.gemm_fp8_block(A, W)])
+for rows in (10, 3000):
+    f = captured(lambda: kl.layer_norm_forward(x[:rows]))
+    same(f, kl.layer_norm_forward(x[:rows]))
+    b = lambda: kl.layer_norm_backward(x[:rows], x[:rows], f[1], f[2])
+    same(captured(b), b())
+h, pos = x[:, None, :512], torch.arange(3000, device="cuda")[:, None]
+same([captured(lambda: kl.rope_axes(h, pos, (256,)))], [kl.rope_axes(h, pos, (256,))])
+assert kl.device_status() == "KL_OK"
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stdout + r.stderr
