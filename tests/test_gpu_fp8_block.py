@@ -99,6 +99,31 @@ def test_encode_nonfinite_blocks_become_nan_and_are_recorded():
     kl.device_status()
 
 
+@pytest.mark.parametrize("R,C", [(6000, 4200), (40000, 600), (1500, 20000), (129, 100003)])
+def test_encode_large_equals_its_parts(R, C):
+    # several words and rows a warp, several tiles a column: as encoded a part at a time
+    x = _x((R, C), R, dtype=torch.bfloat16).cuda()
+    q = kl.quantize_fp8_block(x)
+    for r in (0, 1, R // 2, R - 1):
+        part = kl.quantize_fp8_block(x[r:r + 1])
+        _check_encode(x[r:r + 1], part, "row", False)
+        assert torch.equal(q.codes[r], part.codes[0])
+    lin = kl.quantize_fp8_block(x, layout="linear")
+    assert torch.equal(lin.codes, q.codes)
+    s = kl.quantize_fp8_block(x[128:256], layout="linear").scales
+    assert torch.equal(lin.scales[128:256], s)
+    t = kl.quantize_fp8_block(x, transpose=True, layout="linear")
+    for c in (0, C // 2, C - 1):
+        part = kl.quantize_fp8_block(x[:, c:c + 1].t().contiguous(), layout="linear")
+        assert torch.equal(t.codes[c, :R], part.codes[0, :R]) and torch.equal(t.scales[c], part.scales[0])
+    tile = kl.quantize_fp8_block(x, "tile", layout="linear")
+    last = kl.quantize_fp8_block(x[(R - 1) // 128 * 128:], "tile", layout="linear")
+    assert torch.equal(tile.scales[-1:], last.scales) and torch.equal(tile.codes[-last.rows:], last.codes)
+    tt = kl.quantize_fp8_block(x, "tile", transpose=True, layout="linear")
+    assert torch.equal(tt.scales, tile.scales.t()) and torch.equal(tt.codes[:, :R], tile.codes[:, :C].t())
+    assert kl.device_status() == "KL_OK"
+
+
 def test_codes_past_the_last_column_are_zero_in_nan_blocks_too():
     x = torch.full((20, 37), float("nan"), device="cuda")
     for block, tr in (("row", False), ("row", True), ("tile", False), ("tile", True)):
