@@ -30,6 +30,9 @@ constexpr int kRopeMaxPairs = 256;  // head dim 512
 constexpr int kRopeThreads = 256;
 // rows a thread loads, ahead of as many that it turns and stores
 __host__ __device__ constexpr int rope_batch(int bytes, bool half) { return half && bytes >= 16 ? 2 : 4; }
+// CTAs of a SM: with 16-byte vectors the fourth spills (4,608 x 48 heads, bf16,
+// inputs from HBM: 20.9 us with three, 22.9 with four; 100 dims: 32.7 and 28.4)
+__host__ __device__ constexpr int rope_ctas(int bytes) { return bytes >= 16 ? 3 : 4; }
 constexpr int kRopeTable = 2560;    // (token, pair) entries of a table buffer: two are 40 KB
 
 struct RopeParams {
@@ -151,7 +154,7 @@ struct RopeUnit {
 // heads are spread over the slots, and a thread's rows are one head of tokens
 // `tpar` apart.  Either way a batch of rows lies at one stride.
 template <typename T, int V, bool HALF, bool HEADS>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_axes_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, rope_ctas(V * (int)sizeof(T))) rope_axes_kernel(const __grid_constant__ RopeParams p) {
   constexpr int B = rope_batch(V * (int)sizeof(T), HALF);
   using Unit = RopeUnit<T, V, HALF>;
   extern __shared__ __align__(16) float2 rope_tables[];  // [2][nt][pairs, even] (cos, sin)
@@ -260,10 +263,10 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_axes_kernel(const __grid
 template <typename T, int V>
 static cudaError_t launch_rope_v(RopeParams& p, bool half, cudaStream_t s) {
   p.units = half ? p.pairs / V + (p.dim - 2 * p.pairs) / V : (V == 1 ? (p.dim + 1) / 2 : p.dim / V);
-  // Three CTAs a SM, each of one or a few chunks of tokens within the table:
+  // Three or four CTAs a SM, each of one or a few chunks of tokens within the table:
   // the chunk that leaves the most loaded CTA the fewest tokens.  Fewer tokens
   // than CTAs: one each, and parts of the heads.
-  const int64_t want = (int64_t)device_sm_count() * 3;
+  const int64_t want = (int64_t)device_sm_count() * rope_ctas(V * (int)sizeof(T));
   const int64_t most = kRopeTable / (p.pairs + 1);
   const int64_t chunks_min = p.batch * ((p.tokens + most - 1) / most), rounds0 = (chunks_min + want - 1) / want;
   int64_t nt = 0, least = 0;
@@ -304,8 +307,8 @@ static cudaError_t launch_rope(RopeParams& p, bool half, cudaStream_t s) {
     for (int64_t st : str) ok = ok && st % v == 0;
     return ok;
   };
-  // 3 x 4600 x 20 heads of 100 dims, bf16, in place of single elements: 32.7 us for
-  // 47.7 interleaved, 35.8 for 57.4 half
+  // 3 x 4600 x 20 heads of 100 dims, bf16, in place of single elements: 28.4 us for
+  // 47.7 interleaved, 34.4 for 57.4 half
   if (fits(V)) return launch_rope_v<T, V>(p, half, s);
   return fits(2) ? launch_rope_v<T, 2>(p, half, s) : launch_rope_v<T, 1>(p, half, s);
 }
