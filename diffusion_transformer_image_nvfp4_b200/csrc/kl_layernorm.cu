@@ -1002,11 +1002,11 @@ __global__ void __launch_bounds__(256) ln_param_wide_kernel(const LnParams p) {
 }
 
 // dgain / dbias [groups][cols] from the partial rows, in a fixed order: 32
-// columns a CTA, 16 thread rows taking every 16th partial (148 partials: ten
+// columns a CTA, 32 thread rows taking every 32nd partial (296 partials: ten
 // loads a thread, all in flight at once).
-__global__ void __launch_bounds__(512) ln_param_sum_kernel(const float* __restrict__ part, int splits, int64_t cols,
+__global__ void __launch_bounds__(1024) ln_param_sum_kernel(const float* __restrict__ part, int splits, int64_t cols,
                                                            float* __restrict__ dgain, float* __restrict__ dbias) {
-  __shared__ float red[16][33];
+  __shared__ float red[32][33];
   pdl_wait();
   pdl_trigger();
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;  // of the 2 * cols sums
@@ -1015,13 +1015,13 @@ __global__ void __launch_bounds__(512) ln_param_sum_kernel(const float* __restri
   if (c < 2 * cols) {
     const float* src = part + group * splits * 2 * cols + c;
 #pragma unroll 10
-    for (int i = threadIdx.y; i < splits; i += 16) s += __ldg(src + (int64_t)i * 2 * cols);
+    for (int i = threadIdx.y; i < splits; i += 32) s += __ldg(src + (int64_t)i * 2 * cols);
   }
   red[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && c < 2 * cols) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += red[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) s += red[i][threadIdx.x];
     if (c < cols)
       dgain[group * cols + c] = s;
     else
@@ -1356,7 +1356,7 @@ kl_status kl_layer_norm_backward(const void* dy, int64_t lddy, const void* x, in
                   : dtype == KL_F16 ? launch_ln_backward<__half>(p, vec, s)
                                     : launch_ln_backward<float>(p, vec, s);
   if (e == cudaSuccess && p.part)
-    e = launch_pdl(ln_param_sum_kernel, dim3((unsigned)((2 * cols + 31) / 32), (unsigned)groups), dim3(32, 16), 0, s,
+    e = launch_pdl(ln_param_sum_kernel, dim3((unsigned)((2 * cols + 31) / 32), (unsigned)groups), dim3(32, 32), 0, s,
                    (const float*)p.part, p.splits, cols, dgain, dbias);
   return e == cudaSuccess ? KL_OK : cuda_fail(e);
 }
