@@ -21,7 +21,8 @@
 //
 // B200, bf16, device time: forward 17,408 x 3,072 38.9 us (84% of the 32.6 us its bytes
 // take at the copy's rate); backward 20,992 x 3,072 65.6 us (90% of 59), dx
-// alone 61.  Rows that no vector load suits: 5,000 x 2,047 24.7 and 25.6 us.
+// alone 61.  Rows that 16-byte vectors do not fit: 4,557 x 2,934 18.8 and 24.5
+// us (two elements at a time), 5,000 x 2,047 18.1 and 25.1 (one).
 
 #include <type_traits>
 
@@ -319,9 +320,9 @@ __global__ void __launch_bounds__(256, NV <= (V == 4 ? 24 : 16) ? 2 : 1) ln_forw
   }
 }
 
-// The same for rows that cannot be read as vectors: single elements, the
-// second and third reading of the row from the caches.
-template <typename T>
+// The same for rows that 16-byte vectors do not fit: W = 2 or 1 elements at a
+// time, the second and third reading of the row from the caches.
+template <typename T, int W>
 __global__ void __launch_bounds__(256, 5) ln_forward_warp1_kernel(const LnParams p) {
   extern __shared__ __align__(16) float ln_smem[];  // [gain + plus][bias]
   pdl_wait();
@@ -330,46 +331,77 @@ __global__ void __launch_bounds__(256, 5) ln_forward_warp1_kernel(const LnParams
   const int64_t group = blockIdx.x / p.splits, split = blockIdx.x - group * p.splits;
   ln_stage_params<1>(p, group, ln_smem);
   __syncthreads();
-  const float* gp = ln_smem + lane;
+  const float* gp = ln_smem + lane * W;
+  const float* bp = gp + cols;
   const float inv_c = 1.0f / (float)cols;
-  // f(index, value, exists) for the lane's columns, eight loads at a time
+  // f(index, slot, values, exist) for the lane's columns, eight loads at a time
   auto each = [&](const T* x, auto f) {
     int c = 0;
-#pragma unroll 4
-    for (; c + 256 <= cols; c += 256) {
-      T v[8];
+#pragma unroll (W == 1 ? 4 : 2)
+    for (; c + 256 * W <= cols; c += 256 * W) {
+      uint4 q[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = x[c + k * 32];
+      for (int k = 0; k < 8; ++k) q[k] = load_vec<T, W>(x + c + k * 32 * W);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f(c + k * 32, k, to_f32(v[k]), true);
+      for (int k = 0; k < 8; ++k) {
+        float v[W];
+        unpack_vec<T, W>(q[k], v);
+        f(c + k * 32 * W, k, v, true);
+      }
     }
     if (c < cols) {
-      T v[8];
+      uint4 q[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = c + k * 32 + lane < cols ? x[c + k * 32] : from_f32<T>(0.f);
+      for (int k = 0; k < 8; ++k)
+        q[k] = c + (k * 32 + lane) * W < cols ? load_vec<T, W>(x + c + k * 32 * W) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f(c + k * 32, k, to_f32(v[k]), c + k * 32 + lane < cols);
+      for (int k = 0; k < 8; ++k) {
+        float v[W];
+        unpack_vec<T, W>(q[k], v);
+        f(c + k * 32 * W, k, v, c + (k * 32 + lane) * W < cols);
+      }
     }
   };
   for (int64_t lr = split * 8 + (threadIdx.x >> 5); lr < p.group_rows; lr += p.splits * 8) {
     const int64_t row = group * p.group_rows + lr;
-    const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx + lane;
-    T* y = reinterpret_cast<T*>(p.out) + row * p.ldo + lane;
+    const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx + lane * W;
+    T* y = reinterpret_cast<T*>(p.out) + row * p.ldo + lane * W;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    each(x, [&](int, int k, float v, bool) { s[k & 3] += v; });
+    each(x, [&](int, int k, const float (&v)[W], bool) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) s[(k * W + w) & 3] += v[w];
+    });
     const float mean = warp_sum((s[0] + s[1]) + (s[2] + s[3])) * inv_c;
     s[0] = s[1] = s[2] = s[3] = 0.f;
-    each(x, [&](int, int k, float v, bool in) {
-      const float d = in ? v - mean : 0.f;
-      s[k & 3] = fmaf(d, d, s[k & 3]);
+    each(x, [&](int, int k, const float (&v)[W], bool in) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float d = in ? v[w] - mean : 0.f;
+        s[(k * W + w) & 3] = fmaf(d, d, s[(k * W + w) & 3]);
+      }
     });
     const float rstd = 1.0f / sqrtf(warp_sum((s[0] + s[1]) + (s[2] + s[3])) * inv_c + p.eps);
     if (lane == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
     }
-    each(x, [&](int c, int, float v, bool in) {
-      if (in) y[c] = from_f32<T>(fmaf((v - mean) * rstd, gp[c], gp[cols + c]));
+    each(x, [&](int c, int, const float (&v)[W], bool in) {
+      if (in) {
+        float g[W], b[W], o[W];
+        if constexpr (W == 2) {
+          const float2 gq = *reinterpret_cast<const float2*>(gp + c), bq = *reinterpret_cast<const float2*>(bp + c);
+          g[0] = gq.x;
+          g[1] = gq.y;
+          b[0] = bq.x;
+          b[1] = bq.y;
+        } else {
+          g[0] = gp[c];
+          b[0] = bp[c];
+        }
+#pragma unroll
+        for (int w = 0; w < W; ++w) o[w] = fmaf((v[w] - mean) * rstd, g[w], b[w]);
+        store_vec<T, W>(y + c, o);
+      }
     });
   }
 }
@@ -844,9 +876,10 @@ __global__ void __launch_bounds__(TEAMS ? 512 : 384, !TEAMS && NV * 16 / sizeof(
   }
 }
 
-// Rows that cannot be read as vectors: a thread owns every 32nd column of its
-// warp's 32 E, and loads the next tile's values before it works on this one's.
-template <typename T, int E, bool PG>
+// Rows that 16-byte vectors do not fit: a thread owns every 32nd column (W = 1)
+// or pair of columns (W = 2) of its warp's 32 E, two columns a packed pair, and
+// loads the next tile's values before it works on this one's.
+template <typename T, int E, int W, bool PG>
 __global__ void __launch_bounds__(E == 4 ? 768 : 512) ln_backward_tile1_kernel(const LnParams p, int tx) {
   constexpr int R = kLnTileRows;
   extern __shared__ float ln_sums[];  // [team][2][32 E * warps]
@@ -855,7 +888,8 @@ __global__ void __launch_bounds__(E == 4 ? 768 : 512) ln_backward_tile1_kernel(c
   pdl_trigger();
   const int teams = blockDim.x / tx, team = threadIdx.x / tx, tid = threadIdx.x - team * tx;
   const int warp = tid >> 5, lane = tid & 31, nw = tx >> 5;
-  const int cols = (int)p.cols, c0 = warp * 32 * E + lane;
+  constexpr int H = W == 2 ? 1 : 32;  // from a pair's first column to its second; pairs are 64 apart
+  const int cols = (int)p.cols, c0 = warp * 32 * E + lane * W;
   const bool full = (warp + 1) * 32 * E <= cols;  // every column of the warp exists
   const int group = blockIdx.x / p.splits, split = (blockIdx.x - group * p.splits) * teams + team;
   const int step = p.splits * teams, rows = (int)p.group_rows, tiles = (rows - 1) / R + 1;
@@ -866,12 +900,25 @@ __global__ void __launch_bounds__(E == 4 ? 768 : 512) ln_backward_tile1_kernel(c
 #pragma unroll
   for (int k = 0; k < E / 2; ++k) {
     float ga[1], gb[1];
-    const int a = c0 + 64 * k, b = a + 32;
+    const int a = c0 + 64 * k, b = a + H;
     ln_factor<1>(p, (int64_t)group * cols + a, a < cols, ga);
     ln_factor<1>(p, (int64_t)group * cols + b, b < cols, gb);
     col.g[k] = pack_f32x2(ga[0], gb[0]);
   }
-  T rx[R][E], rd[R][E];
+  // as stored: an element, or the words of a pair
+  using Raw = std::conditional_t<W == 1, T, std::conditional_t<sizeof(T) == 4, uint2, uint32_t>>;
+  Raw rx[R][E / W], rd[R][E / W];
+  auto values = [](const Raw* q, float (&v)[2]) {
+    if constexpr (W == 1) {
+      v[0] = to_f32(q[0]);
+      v[1] = to_f32(q[1]);
+    } else if constexpr (sizeof(T) == 4) {
+      v[0] = __uint_as_float(q->x);
+      v[1] = __uint_as_float(q->y);
+    } else {
+      unpack2<T>(*q, v[0], v[1]);
+    }
+  };
   float next_mean = 0.f, next_rstd = 0.f;  // lane r: row r's
   auto fetch = [&](int tile) {
 #pragma unroll
@@ -882,16 +929,16 @@ __global__ void __launch_bounds__(E == 4 ? 768 : 512) ln_backward_tile1_kernel(c
       const T* d = reinterpret_cast<const T*>(p.dy) + row * p.ldy + c0;
       if (live && full) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          rx[r][k] = x[32 * k];
-          rd[r][k] = d[32 * k];
+        for (int k = 0; k < E / W; ++k) {
+          rx[r][k] = *reinterpret_cast<const Raw*>(x + 32 * W * k);
+          rd[r][k] = *reinterpret_cast<const Raw*>(d + 32 * W * k);
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const bool in = live && c0 + 32 * k < cols;
-          rx[r][k] = in ? x[32 * k] : from_f32<T>(0.f);
-          rd[r][k] = in ? d[32 * k] : from_f32<T>(0.f);
+        for (int k = 0; k < E / W; ++k) {
+          const bool in = live && c0 + 32 * W * k < cols;
+          rx[r][k] = in ? *reinterpret_cast<const Raw*>(x + 32 * W * k) : Raw{};
+          rd[r][k] = in ? *reinterpret_cast<const Raw*>(d + 32 * W * k) : Raw{};
         }
       }
     }
@@ -912,8 +959,11 @@ __global__ void __launch_bounds__(E == 4 ? 768 : 512) ln_backward_tile1_kernel(c
       rs[r] = __shfl_sync(0xffffffffu, next_rstd, r);
 #pragma unroll
       for (int k = 0; k < E / 2; ++k) {
-        x[r][k] = pack_f32x2(to_f32(rx[r][2 * k]), to_f32(rx[r][2 * k + 1]));
-        d[r][k] = pack_f32x2(to_f32(rd[r][2 * k]), to_f32(rd[r][2 * k + 1]));
+        float xv[2], dv[2];
+        values(&rx[r][k * (2 / W)], xv);
+        values(&rd[r][k * (2 / W)], dv);
+        x[r][k] = pack_f32x2(xv[0], xv[1]);
+        d[r][k] = pack_f32x2(dv[0], dv[1]);
       }
     }
     if (tile + step < tiles) fetch(tile + step);
@@ -930,10 +980,14 @@ __global__ void __launch_bounds__(E == 4 ? 768 : 512) ln_backward_tile1_kernel(c
         T* dx = reinterpret_cast<T*>(p.out) + (r0 + tile * R + r) * p.ldo + c0;
 #pragma unroll
         for (int k = 0; k < E / 2; ++k) {
-          float lo, hi;
-          unpack_f32x2(o[k], lo, hi);
-          if (full || c0 + 64 * k < cols) dx[64 * k] = from_f32<T>(lo);
-          if (full || c0 + 64 * k + 32 < cols) dx[64 * k + 32] = from_f32<T>(hi);
+          float v[2];
+          unpack_f32x2(o[k], v[0], v[1]);
+          if constexpr (W == 2) {
+            if (full || c0 + 64 * k < cols) store_vec<T, 2>(dx + 64 * k, v);
+          } else {
+            if (full || c0 + 64 * k < cols) dx[64 * k] = from_f32<T>(v[0]);
+            if (full || c0 + 64 * k + H < cols) dx[64 * k + H] = from_f32<T>(v[1]);
+          }
         }
       }
     }
@@ -943,8 +997,8 @@ __global__ void __launch_bounds__(E == 4 ? 768 : 512) ln_backward_tile1_kernel(c
     float* sums = ln_sums + team * 2 * width + c0;
 #pragma unroll
     for (int k = 0; k < E / 2; ++k) {
-      unpack_f32x2(col.sg[k], sums[64 * k], sums[64 * k + 32]);
-      unpack_f32x2(col.sb[k], sums[width + 64 * k], sums[width + 64 * k + 32]);
+      unpack_f32x2(col.sg[k], sums[64 * k], sums[64 * k + H]);
+      unpack_f32x2(col.sb[k], sums[width + 64 * k], sums[width + 64 * k + H]);
     }
     ln_join_teams(ln_sums, teams, width, cols, p.part + (int64_t)blockIdx.x * 2 * p.cols);
   }
@@ -1119,6 +1173,12 @@ static LnTile ln_tile(int64_t groups, int64_t group_rows, int64_t cols, int es, 
   return t;
 }
 
+// every row of x, dy and the output starts on two elements, and has an even number
+static bool ln_pairs(const LnParams& p, size_t es) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.dy) | reinterpret_cast<uintptr_t>(p.out);
+  return p.cols % 2 == 0 && at % (2 * es) == 0 && p.ldx % 2 == 0 && p.ldy % 2 == 0 && p.ldo % 2 == 0;
+}
+
 template <typename T, int V, int NV>
 static cudaError_t launch_ln_forward_nv(const LnParams& p, const LnShape& sh, cudaStream_t s) {
   return launch_pdl(ln_forward_kernel<T, V, NV>, dim3((unsigned)((p.rows + sh.ty - 1) / sh.ty)), dim3(sh.tx, sh.ty),
@@ -1154,10 +1214,10 @@ static cudaError_t launch_ln_forward(LnParams& p, bool vec, cudaStream_t s) {
     } else if (p.cols <= 6144) {
       const size_t smem = (size_t)p.cols * 8;
       p.splits = (int)ln_ctas(groups, p.group_rows, kNumSMs * 5, 8);
-      const cudaError_t e =
-          cudaFuncSetAttribute(ln_forward_warp1_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 6144 * 8);
+      auto kern = ln_pairs(p, sizeof(T)) ? ln_forward_warp1_kernel<T, 2> : ln_forward_warp1_kernel<T, 1>;
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 6144 * 8);
       if (e != cudaSuccess) return e;
-      return launch_pdl(ln_forward_warp1_kernel<T>, dim3((unsigned)(groups * p.splits)), dim3(256), smem, s, p);
+      return launch_pdl(kern, dim3((unsigned)(groups * p.splits)), dim3(256), smem, s, p);
     }
   }
   const LnShape sh = ln_shape(p.cols, sizeof(T), vec, false);
@@ -1205,8 +1265,9 @@ static cudaError_t launch_ln_tiles(const LnParams& p, const LnTile& t, bool vec,
   if (!vec) {
     const dim3 grid((unsigned)(p.rows / p.group_rows * p.splits)), block(t.tx * t.teams);
     const size_t smem = PG ? (size_t)t.teams * t.tx * 2 * t.n * sizeof(float) : 0;  // at most 32 KB
-    return t.n == 4 ? launch_pdl(ln_backward_tile1_kernel<T, 4, PG>, grid, block, smem, s, p, t.tx)
-                    : launch_pdl(ln_backward_tile1_kernel<T, 8, PG>, grid, block, smem, s, p, t.tx);
+    auto kern = ln_pairs(p, sizeof(T)) ? (t.n == 4 ? ln_backward_tile1_kernel<T, 4, 2, PG> : ln_backward_tile1_kernel<T, 8, 2, PG>)
+                                       : (t.n == 4 ? ln_backward_tile1_kernel<T, 4, 1, PG> : ln_backward_tile1_kernel<T, 8, 1, PG>);
+    return launch_pdl(kern, grid, block, smem, s, p, t.tx);
   }
   if (t.n == 1) return t.tx <= 192 ? launch_ln_tile<T, 1, PG, true>(p, t, s) : launch_ln_tile<T, 1, PG, false>(p, t, s);
   if constexpr (sizeof(T) == 4) {

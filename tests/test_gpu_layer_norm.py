@@ -136,6 +136,21 @@ def test_staged_tiles_of_rows(R, C, groups):
     assert kl.device_status() == "KL_OK"
 
 
+@pytest.mark.parametrize("R,C,groups", [(1205, 258, 1), (2402, 1022, 2), (1501, 1026, 1), (1210, 4094, 2), (900, 2934, 3),
+                                        (700, 6142, 1), (3000, 34, 2)])
+def test_many_rows_of_even_width(R, C, groups):
+    # two elements at a time where x, dy and the results start on them, else one
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        wide = _randn((R, C + 3), 1, dtype, 2.0, 1.0)
+        gain, bias = _params("gain", groups, C, torch.float32, 3)
+        for x in (wide[:, 2:C + 2].contiguous(), wide[:, 1:C + 1]):
+            y, mean, rstd = kl.layer_norm_forward(x, gain, bias)
+            _check_forward(y, mean, rstd, x, gain, bias, False)
+            dy = _randn((R, C), 2, dtype)
+            got = kl.layer_norm_backward(dy, x, mean, rstd, gain)
+            _check_backward(got, dy, x, mean, rstd, gain, False, groups)
+
+
 @pytest.mark.parametrize("R,C,groups", [(1205, 257, 1), (2402, 1023, 2), (1501, 1025, 1), (1210, 4095, 2), (900, 2047, 3),
                                         (700, 6143, 1), (3000, 33, 2)])
 def test_many_rows_of_odd_width(R, C, groups):
