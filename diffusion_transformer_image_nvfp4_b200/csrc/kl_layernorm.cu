@@ -22,7 +22,8 @@
 // B200, bf16, device time: forward 17,408 x 3,072 38.9 us (84% of the 32.6 us its bytes
 // take at the copy's rate); backward 20,992 x 3,072 65.6 us (90% of 59), dx
 // alone 61.  Rows that 16-byte vectors do not fit: 4,557 x 2,934 18.8 and 24.5
-// us (two elements at a time), 5,000 x 2,047 18.1 and 25.1 (one).
+// us (two elements at a time; 25.6 and 33.3 with one), 5,000 x 2,047 18.1 and
+// 25.1 (one).
 
 #include <type_traits>
 
