@@ -343,7 +343,8 @@ extern "C" kl_status kl_rope_axes(const kl_rope_args* r, void* stream) {
   // no output element twice; in place only element by element
   const int64_t size[3] = {r->batch, r->tokens, r->heads};
   for (int i = 0; i < 3; ++i)
-    if (size[i] > 1 && (r->out_stride[i] == 0 || (r->x == r->out && r->x_stride[i] != r->out_stride[i])))
+    if (size[i] > 1 && ((r->out_stride[i] < r->dim && r->out_stride[i] > -r->dim) ||
+                        (r->x == r->out && r->x_stride[i] != r->out_stride[i])))
       return KL_ERR_INVALID_ARG;
   kl_status st = check_arch();
   if (st != KL_OK) return st;

@@ -701,7 +701,8 @@ kl_status kl_gemm_fp8_block(const kl_fp8_tensor* A, const kl_fp8_tensor* W, int6
  * Strides (batch, token, head) are in elements, dims are consecutive; dim <=
  * 512.  pos: int32, int64 or fp32 [batch, tokens, naxes] consecutive, or
  * [tokens, naxes] for every batch with pos_shared.  out may be x itself with
- * the same strides (in place); otherwise they must not overlap.
+ * the same strides (in place); otherwise they must not overlap, nor the heads of
+ * out one another.
  */
 #define KL_ROPE_MAX_AXES 4
 #define KL_ROPE_HALF 1

@@ -80,6 +80,7 @@ def test_rope_refusals(L):
 
     # (x is out here) in place at other strides; an output that is broadcast
     assert r(out_stride=st(0, 256, 127)) == r(x_stride=st(0, 0, 128)) == INVALID
+    assert r(out=2 * FAKE, out_stride=st(0, 256, 100)) == r(out=2 * FAKE, out_stride=st(0, -127, 128)) == INVALID
     assert r(out=2 * FAKE, out_stride=st(0, 0, 128)) == r(out=2 * FAKE, batch=2, out_stride=st(0, 256, 128)) == INVALID
     assert r(x=FAKE + 1) == r(out=FAKE + 1) == r(pos=FAKE + 2) == r(pos=FAKE + 4, pos_type=1) == MISALIGNED
 
