@@ -17,7 +17,8 @@
 // Backward: a thread meets the same columns in every row of its CTA, so the
 // sums for dgain and dbias stay in its registers; CTAs walk the rows of one
 // group with a fixed stride and leave one partial row each, which a second
-// kernel adds in a fixed order -- no atomics, the same bits every run.
+// kernel adds in a fixed order -- no atomics, the same bits every run.  Few
+// rows: one launch, whose other CTAs add the columns from x and dy themselves.
 //
 // B200, bf16, device time: forward 17,408 x 3,072 38.9 us (84% of the 32.6 us its bytes
 // take at the copy's rate); backward 20,992 x 3,072 65.6 us (90% of 59), dx

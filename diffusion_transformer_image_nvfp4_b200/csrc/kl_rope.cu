@@ -4,9 +4,8 @@
 //
 // Pair j of a head turns by pos[token, axis(j)] * f_j: the pairs are divided
 // among the axes in order (`sections`), f_j = theta^(-u / n_a) with u the
-// pair's index in its axis' section of n_a pairs (KL_ROPE_LADDER_AXIS), or
-// theta^(-j / P) over all P pairs (KL_ROPE_LADDER_SHARED).  Dims past the
-// pairs are copied.
+// pair's index in its axis' section of n_a pairs, or theta^(-j / P) over all
+// P pairs (KL_ROPE_LADDER_SHARED).  Dims past the pairs are copied.
 //
 // Angles: f_j / pi is made on the host in extended precision; position times
 // it is one fp64 product, reduced by whole turns exactly (h - 2 rint(h / 2)),
@@ -17,7 +16,9 @@
 // few chunks of tokens; two table buffers leave one barrier a chunk.
 //
 // Bound by HBM: one read and one write of the tensor; the fp64 work is one
-// angle per (token, pair), a head's share of it 1 / H.
+// angle per (token, pair), a head's share of it 1 / H.  B200, device time, bf16,
+// 48 heads of 128: 4,608 tokens 22.2 us (78% of the copy's rate), 20,992 87.8
+// (89%); fp32, 2 x 3,315 x 6 heads of 96 7.3.
 #include <cmath>
 
 #include "../../include/klein.h"
