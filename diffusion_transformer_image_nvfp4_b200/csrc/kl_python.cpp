@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
 #include "../../include/klein.h"
@@ -105,6 +106,13 @@ PyObject* tuple(std::initializer_list<at::Tensor> ts) {
     PyTuple_SET_ITEM(r, i++, o);
   }
   return r;
+}
+
+// A caller's tensor has been written: its version moves on, as for torch's own
+// writes in place, so that autograd refuses to use values it saved from before.
+// (Inference tensors have no version and are never saved.)
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) torch::autograd::impl::bump_version(t);
 }
 
 // f(stream) with the tensors' device current
@@ -199,6 +207,7 @@ if (a[7] == Py_None) {
 }
 call(dev, "kl_gemm_fp8_block",
      [&](void* s) { return kl_gemm_fp8_block(&A, &W, M, N, K, out.data_ptr(), type, ldo, kernel, s); });
+if (a[7] != Py_None) written(out);
 return wrap(std::move(out));
 KL_METHOD_END
 
@@ -256,6 +265,7 @@ r.x = x.data_ptr();
 r.out = out.data_ptr();
 r.pos = pos.data_ptr();
 call(dev, "kl_rope_axes", [&](void* s) { return kl_rope_axes(&r, s); });
+if (a[5] != Py_None) written(out);
 return wrap(std::move(out));
 KL_METHOD_END
 
