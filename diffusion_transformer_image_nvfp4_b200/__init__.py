@@ -680,7 +680,9 @@ def dit_step_cached(shape, weights, cache, threshold, latent, text, mod_mode, mo
 # These calls run on the current stream of their tensors' device, whichever
 # device is current, and allocate outputs and scratch per call.  They go
 # through the compiled binding: from here they would cost more of the CPU than
-# the small ones take on the GPU.
+# the small ones take on the GPU.  None records an autograd graph: with grad
+# mode on, a tensor that requires a gradient is refused (ValueError); the
+# backward forms are for a torch.autograd.Function, or for use by hand.
 KL_FP8_TILE, KL_FP8_TRANSPOSE = 16, 32
 FP8_GEMM_KERNELS = {"auto": 0, "pair_256x256": 1, "pair_256x128": 2, "split": 3}
 _OUT_TYPE = {torch.bfloat16: KL_OUT_BF16, torch.float32: KL_OUT_F32}

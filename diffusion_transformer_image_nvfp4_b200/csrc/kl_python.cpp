@@ -9,6 +9,7 @@
 // other than KL_OK becomes a KLError.  Nothing is kept between calls.
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -25,7 +26,12 @@ PyObject* g_error = nullptr;  // KLError(status, where)
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
   TORCH_CHECK_VALUE(THPVariable_Check(o), name, ": expected a CUDA tensor");
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  // results carry no graph: with grad mode on, one would be cut without a word
+  TORCH_CHECK_VALUE(!(t.requires_grad() && at::GradMode::is_enabled()), name,
+                    ": requires a gradient, which this call does not record; pass it detached, or call under "
+                    "torch.no_grad() or from a torch.autograd.Function");
+  return t;
 }
 int64_t integer(PyObject* o) {
   const int64_t v = PyLong_AsLongLong(o);
