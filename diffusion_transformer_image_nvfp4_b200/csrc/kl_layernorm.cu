@@ -21,10 +21,10 @@
 // rows: one launch, whose other CTAs add the columns from x and dy themselves.
 //
 // B200, bf16, device time: forward 17,408 x 3,072 38.9 us (84% of the 32.6 us its bytes
-// take at the copy's rate); backward 20,992 x 3,072 65.6 us (90% of 59), dx
-// alone 61.  Rows that 16-byte vectors do not fit: 4,557 x 2,934 18.8 and 24.5
+// take at the copy's rate); backward 20,992 x 3,072 65.9 us (89% of 59), dx
+// alone 61.7.  Rows that 16-byte vectors do not fit: 4,557 x 2,934 18.8 and 24.1
 // us (two elements at a time; 25.6 and 33.3 with one), 5,000 x 2,047 18.1 and
-// 25.1 (one).
+// 23.0 (one).
 
 #include <type_traits>
 
@@ -675,8 +675,11 @@ struct LnColumns {
       for (int k = 0; k < E / 2; ++k) sg[k] = sb[k] = 0;
     }
   }
-  // x, dy of the rows -> x - mean and dy; the thread's part of the row sums of
-  // h and h (x - mean).  Columns and rows that do not exist hold dy = 0.
+  // x, dy of the rows -> xhat and dy; the thread's part of the row sums of h
+  // and h xhat.  (xhat first, as in the kernels above: dy (x - mean) leaves the
+  // range of fp32 where dy xhat does not.)  A column that does not exist holds
+  // dy = 0, and the mean or an existing column's x: the xhat of anything else
+  // might not be finite.  A row that does not exist holds zeros.
   __device__ __forceinline__ void sums(uint64_t (&x)[R][E / 2], const uint64_t (&d)[R][E / 2], const float (&m)[R],
                                        const float (&rs)[R], float (&s)[2 * R]) {
 #pragma unroll
@@ -685,10 +688,10 @@ struct LnColumns {
       uint64_t s0 = 0, s1 = 0;
 #pragma unroll
       for (int k = 0; k < E / 2; ++k) {
-        x[r][k] = add_f32x2(x[r][k], nm2);
-        const uint64_t u = mul_f32x2(d[r][k], x[r][k]);  // dy * xhat / rstd
+        x[r][k] = mul_f32x2(add_f32x2(x[r][k], nm2), rs2);
+        const uint64_t u = mul_f32x2(d[r][k], x[r][k]);  // dy * xhat
         if constexpr (PG) {
-          sg[k] = fma_f32x2(u, rs2, sg[k]);
+          sg[k] = add_f32x2(sg[k], u);
           sb[k] = add_f32x2(sb[k], d[r][k]);
         }
         s0 = fma_f32x2(d[r][k], g[k], s0);
@@ -716,11 +719,10 @@ struct LnColumns {
     tot[2] = hi ? b2 : b;
     tot[3] = hi ? b : b2;
   }
-  // dx = rs * (h - mean(h) - (x - m) * rs * (rs * mean(h (x - m)))) of row r
+  // dx = rs * (h - mean(h) - xhat * mean(h xhat)) of row r
   __device__ __forceinline__ void dx(const uint64_t (&x)[E / 2], const uint64_t (&d)[E / 2], float rs, float mh,
                                      float mhx, uint64_t (&o)[E / 2]) const {
-    const float a = -rs * (rs * mhx);
-    const uint64_t a2 = pack_f32x2(a, a), b2 = pack_f32x2(-mh, -mh), rs2 = pack_f32x2(rs, rs);
+    const uint64_t a2 = pack_f32x2(-mhx, -mhx), b2 = pack_f32x2(-mh, -mh), rs2 = pack_f32x2(rs, rs);
 #pragma unroll
     for (int k = 0; k < E / 2; ++k) o[k] = mul_f32x2(rs2, fma_f32x2(d[k], g[k], fma_f32x2(x[k], a2, b2)));
   }
@@ -812,7 +814,8 @@ __global__ void __launch_bounds__(TEAMS ? 512 : 384, !TEAMS && NV * 16 / sizeof(
       for (int i = 0; i < NV; ++i) {
         const int at = tid + i * tx;
         const bool in = r < n && at * V < cols;
-        const uint4 qx = in ? *reinterpret_cast<const uint4*>(xs + r * row_bytes + at * 16) : make_uint4(0, 0, 0, 0);
+        const uint4 qx = r < n ? *reinterpret_cast<const uint4*>(xs + r * row_bytes + (at * V < cols ? at : 0) * 16)
+                               : make_uint4(0, 0, 0, 0);
         const uint4 qd =
             in ? *reinterpret_cast<const uint4*>(xs + half + r * row_bytes + at * 16) : make_uint4(0, 0, 0, 0);
         unpack_vec2<T, V>(qx, *reinterpret_cast<uint64_t(*)[V / 2]>(&x[r][i * V / 2]));
@@ -921,79 +924,95 @@ __global__ void __launch_bounds__(E == 4 ? 768 : 512) ln_backward_tile1_kernel(c
       unpack2<T>(*q, v[0], v[1]);
     }
   };
-  float next_mean = 0.f, next_rstd = 0.f;  // lane r: row r's
-  auto fetch = [&](int tile) {
+  // One copy of the loop for warps that have all their columns: with what the
+  // others need in it, 4,557 x 2,934 bf16 took 30.9 us in place of 24.1.  In
+  // place of the x of columns that do not exist (LnColumns::sums) pairs read the
+  // row's first and single elements take the mean: 5,000 x 4,001 fp32 49.4 us,
+  // 55.4 the other way; 4,557 x 2,934 bf16, dx alone, 20.9 and 25.5.
+  auto walk = [&](auto whole) {
+    constexpr bool FULL = decltype(whole)::value;
+    float next_mean = 0.f, next_rstd = 0.f;  // lane r: row r's
+    auto fetch = [&](int tile) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool live = tile * R + r < rows;
-      const int64_t row = r0 + (live ? tile * R + r : 0);
-      const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx + c0;
-      const T* d = reinterpret_cast<const T*>(p.dy) + row * p.ldy + c0;
-      if (live && full) {
+      for (int r = 0; r < R; ++r) {
+        const bool live = tile * R + r < rows;
+        const int64_t row = r0 + (live ? tile * R + r : 0);
+        const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx + c0;
+        const T* d = reinterpret_cast<const T*>(p.dy) + row * p.ldy + c0;
+        if (live) {
 #pragma unroll
-        for (int k = 0; k < E / W; ++k) {
-          rx[r][k] = *reinterpret_cast<const Raw*>(x + 32 * W * k);
-          rd[r][k] = *reinterpret_cast<const Raw*>(d + 32 * W * k);
-        }
-      } else {
+          for (int k = 0; k < E / W; ++k) {
+            const bool in = FULL || c0 + 32 * W * k < cols;
+            if constexpr (W == 2)
+              rx[r][k] = *reinterpret_cast<const Raw*>(x + (in ? 64 * k : -c0));
+            else
+              rx[r][k] = in ? *reinterpret_cast<const Raw*>(x + 32 * k) : Raw{};
+            rd[r][k] = in ? *reinterpret_cast<const Raw*>(d + 32 * W * k) : Raw{};
+          }
+        } else {
 #pragma unroll
-        for (int k = 0; k < E / W; ++k) {
-          const bool in = live && c0 + 32 * W * k < cols;
-          rx[r][k] = in ? *reinterpret_cast<const Raw*>(x + 32 * W * k) : Raw{};
-          rd[r][k] = in ? *reinterpret_cast<const Raw*>(d + 32 * W * k) : Raw{};
+          for (int k = 0; k < E / W; ++k) rx[r][k] = rd[r][k] = Raw{};
         }
       }
-    }
-    const int lr = tile * R + lane;
-    const bool in = lane < R && lr < rows;
-    next_mean = in ? __ldg(p.mean + r0 + lr) : 0.f;
-    next_rstd = in ? __ldg(p.rstd + r0 + lr) : 0.f;
-  };
-  if (split < tiles) fetch(split);
-  int buf = 0;
-  for (int tile = split; tile < tiles; tile += step, buf ^= 1) {
-    const int n = min(R, rows - tile * R);
-    float m[R], rs[R];
-    uint64_t x[R][E / 2], d[R][E / 2];
+      const int lr = tile * R + lane;
+      const bool in = lane < R && lr < rows;
+      next_mean = in ? __ldg(p.mean + r0 + lr) : 0.f;
+      next_rstd = in ? __ldg(p.rstd + r0 + lr) : 0.f;
+    };
+    if (split < tiles) fetch(split);
+    int buf = 0;
+    for (int tile = split; tile < tiles; tile += step, buf ^= 1) {
+      const int n = min(R, rows - tile * R);
+      float m[R], rs[R];
+      uint64_t x[R][E / 2], d[R][E / 2];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      m[r] = __shfl_sync(0xffffffffu, next_mean, r);
-      rs[r] = __shfl_sync(0xffffffffu, next_rstd, r);
-#pragma unroll
-      for (int k = 0; k < E / 2; ++k) {
-        float xv[2], dv[2];
-        values(&rx[r][k * (2 / W)], xv);
-        values(&rd[r][k * (2 / W)], dv);
-        x[r][k] = pack_f32x2(xv[0], xv[1]);
-        d[r][k] = pack_f32x2(dv[0], dv[1]);
-      }
-    }
-    if (tile + step < tiles) fetch(tile + step);
-    float s[2 * R], tot[2 * R];
-    col.sums(x, d, m, rs, s);
-    if (lane < 2 * R) red[team][buf][warp][lane] = s[0];
-    team_sync(team, tx);
-    col.join(&red[team][buf][0][0], nw, tot);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r < n) {
-        uint64_t o[E / 2];
-        col.dx(x[r], d[r], rs[r], tot[2 * r] * inv_c, tot[2 * r + 1] * inv_c, o);
-        T* dx = reinterpret_cast<T*>(p.out) + (r0 + tile * R + r) * p.ldo + c0;
+      for (int r = 0; r < R; ++r) {
+        m[r] = __shfl_sync(0xffffffffu, next_mean, r);
+        rs[r] = __shfl_sync(0xffffffffu, next_rstd, r);
 #pragma unroll
         for (int k = 0; k < E / 2; ++k) {
-          float v[2];
-          unpack_f32x2(o[k], v[0], v[1]);
-          if constexpr (W == 2) {
-            if (full || c0 + 64 * k < cols) store_vec<T, 2>(dx + 64 * k, v);
-          } else {
-            if (full || c0 + 64 * k < cols) dx[64 * k] = from_f32<T>(v[0]);
-            if (full || c0 + 64 * k + H < cols) dx[64 * k + H] = from_f32<T>(v[1]);
+          float xv[2], dv[2];
+          values(&rx[r][k * (2 / W)], xv);
+          values(&rd[r][k * (2 / W)], dv);
+          if constexpr (!FULL && W == 1) {
+            if (c0 + 64 * k >= cols) xv[0] = m[r];
+            if (c0 + 64 * k + H >= cols) xv[1] = m[r];
+          }
+          x[r][k] = pack_f32x2(xv[0], xv[1]);
+          d[r][k] = pack_f32x2(dv[0], dv[1]);
+        }
+      }
+      if (tile + step < tiles) fetch(tile + step);
+      float s[2 * R], tot[2 * R];
+      col.sums(x, d, m, rs, s);
+      if (lane < 2 * R) red[team][buf][warp][lane] = s[0];
+      team_sync(team, tx);
+      col.join(&red[team][buf][0][0], nw, tot);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r < n) {
+          uint64_t o[E / 2];
+          col.dx(x[r], d[r], rs[r], tot[2 * r] * inv_c, tot[2 * r + 1] * inv_c, o);
+          T* dx = reinterpret_cast<T*>(p.out) + (r0 + tile * R + r) * p.ldo + c0;
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) {
+            float v[2];
+            unpack_f32x2(o[k], v[0], v[1]);
+            if constexpr (W == 2) {
+              if (FULL || c0 + 64 * k < cols) store_vec<T, 2>(dx + 64 * k, v);
+            } else {
+              if (FULL || c0 + 64 * k < cols) dx[64 * k] = from_f32<T>(v[0]);
+              if (FULL || c0 + 64 * k + H < cols) dx[64 * k + H] = from_f32<T>(v[1]);
+            }
           }
         }
       }
     }
-  }
+  };
+  if (full)
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
   if constexpr (PG) {
     const int width = nw * 32 * E;
     float* sums = ln_sums + team * 2 * width + c0;
