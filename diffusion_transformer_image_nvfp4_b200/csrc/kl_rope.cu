@@ -20,6 +20,7 @@
 // 48 heads of 128: 4,608 tokens 22.2 us (78% of the copy's rate), 20,992 87.8
 // (89%); fp32, 2 x 3,315 x 6 heads of 96 7.3.
 #include <cmath>
+#include <utility>
 
 #include "../../include/klein.h"
 #include "kl_common.cuh"
@@ -314,6 +315,53 @@ static cudaError_t launch_rope(RopeParams& p, bool half, cudaStream_t s) {
   return fits(2) ? launch_rope_v<T, 2>(p, half, s) : launch_rope_v<T, 1>(p, half, s);
 }
 
+// Two of the size[0] x size[1] x size[2] heads of `dim` elements share one.
+// Strides that nest (each at least what the smaller ones span) cannot; others
+// are searched: over the differences of two of the indices, the third's is the
+// quotient.  Past kSearch differences (a millisecond) the answer is yes.
+static bool rope_heads_overlap(const int64_t (&size)[3], const int64_t (&stride)[3], int64_t dim) {
+  using wide = __int128;
+  constexpr wide kSearch = 1 << 16;
+  int64_t n[3], st[3];
+  int m = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] == 1) continue;
+    n[m] = size[i] - 1;  // the largest difference of two indices
+    if (stride[i] == INT64_MIN) return true;
+    st[m++] = stride[i] < 0 ? -stride[i] : stride[i];
+  }
+  for (int i = 1; i < m; ++i)  // by stride
+    for (int j = i; j > 0 && st[j] < st[j - 1]; --j) {
+      std::swap(st[j], st[j - 1]);
+      std::swap(n[j], n[j - 1]);
+    }
+  wide span = dim;
+  bool nested = true;
+  for (int i = 0; i < m; ++i) {
+    nested = nested && st[i] >= span;
+    span += (wide)n[i] * st[i];
+  }
+  if (nested) return false;
+  if (m == 1) return true;  // a stride below dim
+  for (int i = 0; i < m; ++i)
+    if (st[i] < dim) return true;
+  int k = 0;  // the index solved for: the longest
+  for (int i = 1; i < m; ++i)
+    if (n[i] > n[k]) k = i;
+  const int a = k == 0 ? 1 : 0, b = m == 3 ? 3 - k - a : -1;
+  const int64_t nb = b >= 0 ? n[b] : 0, sb = b >= 0 ? st[b] : 0;
+  if (((wide)n[a] + 1) * (2 * (wide)nb + 1) > kSearch) return true;
+  for (int64_t i = 0; i <= n[a]; ++i)
+    for (int64_t j = i == 0 ? 1 : -nb; j <= nb; ++j) {
+      // a multiple q st[k], |q| <= n[k], within dim of this difference's opposite
+      const wide at = (wide)i * st[a] + (wide)j * sb, mag = at < 0 ? -at : at;
+      wide q = (mag + dim - 1) / st[k];  // the largest with q st[k] < mag + dim
+      if (q > n[k]) q = n[k];
+      if (q * st[k] > mag - dim) return true;
+    }
+  return false;
+}
+
 }  // namespace kl
 
 extern "C" kl_status kl_rope_axes(const kl_rope_args* r, void* stream) {
@@ -338,15 +386,14 @@ extern "C" kl_status kl_rope_axes(const kl_rope_args* r, void* stream) {
   const int64_t lim = (int64_t)1 << 31;
   if (r->batch >= lim || r->tokens >= lim || r->heads >= lim / 2 || r->batch > lim / r->tokens)
     return KL_ERR_UNSUPPORTED_SHAPE;
+  // no output element twice; in place only element by element
+  const int64_t size[3] = {r->batch, r->tokens, r->heads};
+  if (rope_heads_overlap(size, r->out_stride, r->dim)) return KL_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (size[i] > 1 && r->x == r->out && r->x_stride[i] != r->out_stride[i]) return KL_ERR_INVALID_ARG;
   const int es = r->dtype == KL_F32 ? 4 : 2;
   if (!aligned(r->x, es) || !aligned(r->out, es) || !aligned(r->pos, r->pos_type == KL_POS_I64 ? 8 : 4))
     return KL_ERR_MISALIGNED;
-  // no output element twice; in place only element by element
-  const int64_t size[3] = {r->batch, r->tokens, r->heads};
-  for (int i = 0; i < 3; ++i)
-    if (size[i] > 1 && ((r->out_stride[i] < r->dim && r->out_stride[i] > -r->dim) ||
-                        (r->x == r->out && r->x_stride[i] != r->out_stride[i])))
-      return KL_ERR_INVALID_ARG;
   kl_status st = check_arch();
   if (st != KL_OK) return st;
   p.x = r->x;

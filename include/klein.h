@@ -701,8 +701,10 @@ kl_status kl_gemm_fp8_block(const kl_fp8_tensor* A, const kl_fp8_tensor* W, int6
  * Strides (batch, token, head) are in elements, dims are consecutive; dim <=
  * 512.  pos: int32, int64 or fp32 [batch, tokens, naxes] consecutive, or
  * [tokens, naxes] for every batch with pos_shared.  out may be x itself with
- * the same strides (in place); otherwise they must not overlap, nor the heads of
- * out one another.
+ * the same strides (in place); otherwise they must not overlap.  The heads of out
+ * must not overlap one another: refused (KL_ERR_INVALID_ARG), as are strides out
+ * of the common (none within what the smaller ones span) with too many heads to
+ * be sure.
  */
 #define KL_ROPE_MAX_AXES 4
 #define KL_ROPE_HALF 1
