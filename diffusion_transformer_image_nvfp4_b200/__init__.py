@@ -15,7 +15,7 @@ from dataclasses import dataclass
 
 import torch
 
-from .build import BIND_PATH, LIB_PATH
+from .build import LIB_PATH, bind_path
 
 __all__ = [
     "KLError", "lib", "NVFP4", "quantize_nvfp4", "ln_modulate_quantize_nvfp4", "gemm_nvfp4_fused",
@@ -692,14 +692,15 @@ _EXT = None
 
 
 def _ext():
-    """The compiled binding klein_torch.so (raises if it has not been built)."""
+    """The compiled binding (raises if none has been built for this Python and torch)."""
     global _EXT
     if _EXT is None:
         lib()
-        if not os.path.exists(BIND_PATH):
-            raise RuntimeError(f"{BIND_PATH} is missing: build it with "
+        path = bind_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
                                "`python -m diffusion_transformer_image_nvfp4_b200.build`")
-        spec = importlib.util.spec_from_file_location("klein_torch", BIND_PATH)
+        spec = importlib.util.spec_from_file_location("klein_torch", path)
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
         ext.set_error(KLError)

@@ -1,5 +1,7 @@
 """Build libklein.so (the CUDA library) in-tree with nvcc for sm_100a, and
-klein_torch.so (its binding to torch tensors, for the projection path) with g++.
+klein_torch.<ABI>.so (its binding to torch tensors, for the projection path) with
+g++.  The binding's name holds the Python and torch it was compiled against, so
+another of either finds none and has it built.
 
 Usage: ``python -m diffusion_transformer_image_nvfp4_b200.build [--force]``.
 """
@@ -13,7 +15,6 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libklein.so")
-BIND_PATH = os.path.join(PKG_DIR, "klein_torch.so")
 BIND_SOURCE = os.path.join(CSRC, "kl_python.cpp")
 HEADER = os.path.join(ROOT, "include", "klein.h")
 
@@ -29,6 +30,17 @@ def _sources():
     return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if not f.endswith(".cpp")] + [HEADER]
 
 
+def bind_path():
+    """The binding compiled against the running Python and torch."""
+    import sysconfig
+
+    import torch
+
+    abi = "-".join([sysconfig.get_config_var("SOABI"), "torch", torch.__version__, str(torch.version.git_version)[:8],
+                    f"cxx11abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"])
+    return os.path.join(PKG_DIR, f"klein_torch.{abi}.so")
+
+
 def _stale(path, sources):
     return not os.path.exists(path) or any(os.path.getmtime(s) > os.path.getmtime(path) for s in sources)
 
@@ -38,11 +50,11 @@ def needs_build():
 
 
 def build(force=False, verbose=False):
-    """Compile csrc/klein.cu into libklein.so and csrc/kl_python.cpp into
-    klein_torch.so next to this file; returns libklein.so's path."""
+    """Compile csrc/klein.cu into libklein.so and csrc/kl_python.cpp into the
+    binding next to this file; returns libklein.so's path."""
     if force or needs_build():
         _build_lib(verbose)
-    if force or _stale(BIND_PATH, [BIND_SOURCE, HEADER]):
+    if force or _stale(bind_path(), [BIND_SOURCE, HEADER]):
         _build_binding()
     return LIB_PATH
 
@@ -60,7 +72,7 @@ def _build_binding():
 
     import torch
 
-    root = os.path.dirname(torch.__file__)
+    root, path = os.path.dirname(torch.__file__), bind_path()
     inc, cuda = os.path.join(root, "include"), os.path.dirname(os.path.dirname(_nvcc()))
     dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
             sysconfig.get_paths()["include"]]
@@ -68,8 +80,8 @@ def _build_binding():
     # in the binding, which a C++ runtime of its own (linked statically) cannot do
     _run([shutil.which("g++", path="/usr/bin:/usr/local/bin") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in dirs), BIND_SOURCE,
-          "-o", BIND_PATH + ".tmp", f"-L{PKG_DIR}", f"-L{os.path.join(root, 'lib')}", "-l:libklein.so", "-ltorch_python",
-          "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], BIND_PATH)
+          "-o", path + ".tmp", f"-L{PKG_DIR}", f"-L{os.path.join(root, 'lib')}", "-l:libklein.so", "-ltorch_python",
+          "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], path)
 
 
 def _build_lib(verbose):
