@@ -3,7 +3,8 @@ klein_torch.<ABI>.so (its binding to torch tensors, for the projection path) wit
 g++.  The binding's name holds the Python and torch it was compiled against, so
 another of either finds none and has it built.
 
-Usage: ``python -m diffusion_transformer_image_nvfp4_b200.build [--force]``.
+Usage: ``python -m diffusion_transformer_image_nvfp4_b200.build [--force] [--lib-only]``
+(``--lib-only``: no binding, for users of the C ABI; needs nvcc alone).
 """
 
 import os
@@ -49,12 +50,13 @@ def needs_build():
     return _stale(LIB_PATH, _sources())
 
 
-def build(force=False, verbose=False):
-    """Compile csrc/klein.cu into libklein.so and csrc/kl_python.cpp into the
-    binding next to this file; returns libklein.so's path."""
+def build(force=False, verbose=False, binding=True):
+    """Compile csrc/klein.cu into libklein.so and, unless ``binding`` is false,
+    csrc/kl_python.cpp into the binding next to this file; returns libklein.so's
+    path."""
     if force or needs_build():
         _build_lib(verbose)
-    if force or _stale(bind_path(), [BIND_SOURCE, HEADER]):
+    if binding and (force or _stale(bind_path(), [BIND_SOURCE, HEADER])):
         _build_binding()
     return LIB_PATH
 
@@ -102,4 +104,4 @@ def _build_lib(verbose):
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv, binding="--lib-only" not in sys.argv))

@@ -2,6 +2,8 @@
 nor the loader takes it for another."""
 
 import os
+import subprocess
+import sys
 import sysconfig
 
 import pytest
@@ -47,3 +49,27 @@ def test_the_loaded_binding_is_this_abis():
     build.build()
     path = kl._ext().__file__
     assert path == build.bind_path() and torch.__version__ in os.path.basename(path)
+
+
+def test_the_library_is_built_without_the_binding(monkeypatch):
+    # what the C ABI needs does not depend on g++, or on torch's and Python's headers
+    ran = []
+    monkeypatch.setattr(build, "_build_lib", lambda verbose: ran.append("lib"))
+    monkeypatch.setattr(build, "_build_binding", lambda: ran.append("binding"))
+    assert build.build(force=True, binding=False) == build.LIB_PATH and ran == ["lib"]
+    ran.clear()
+    build.build(force=True)
+    assert ran == ["lib", "binding"]
+
+
+def test_lib_only_from_the_command_line():
+    build.build()
+    before = os.stat(build.bind_path()).st_mtime_ns
+    os.utime(build.bind_path(), (1, 1))  # out of date
+    try:
+        r = subprocess.run([sys.executable, "-m", "diffusion_transformer_image_nvfp4_b200.build", "--lib-only"],
+                           capture_output=True, text=True, cwd=build.ROOT)
+        assert r.returncode == 0 and r.stdout.strip() == build.LIB_PATH, r.stderr
+        assert os.stat(build.bind_path()).st_mtime == 1
+    finally:
+        os.utime(build.bind_path(), ns=(before, before))
