@@ -20,36 +20,30 @@ static kl_status cuda_fail(cudaError_t e) {
   return KL_ERR_CUDA;
 }
 
-constexpr int kMaxDevices = 64;
-static int g_sms[kMaxDevices];
-static int g_arch_ok[kMaxDevices];  // 0 unknown, 1 sm_100, -1 other
+static DeviceValue g_sms;
+static DeviceValue g_arch;  // 1 sm_100, -1 other
 
 int device_sm_count() {
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= kMaxDevices) return kNumSMs;
-  if (g_sms[dev] == 0) {
+  return g_sms.get(dev, [dev] {
     int n = 0;
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    g_sms[dev] = n > 0 ? n : kNumSMs;
-  }
-  return g_sms[dev];
+    return n > 0 ? n : kNumSMs;
+  });
 }
 
 static kl_status check_arch() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
-  const bool cached = dev >= 0 && dev < kMaxDevices;  // devices past the cache are asked every time
-  if (!cached || g_arch_ok[dev] == 0) {
+  const int arch = g_arch.get(dev, [dev] {
     int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    const int ok = (major == 10 && minor == 0) ? 1 : -1;
-    if (!cached) return ok == 1 ? KL_OK : KL_ERR_ARCH;
-    g_arch_ok[dev] = ok;
-  }
-  return g_arch_ok[dev] == 1 ? KL_OK : KL_ERR_ARCH;
+    return major == 10 && minor == 0 ? 1 : -1;
+  });
+  return arch == 1 ? KL_OK : KL_ERR_ARCH;
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {

@@ -660,10 +660,10 @@ static double fp8_pair_time(const GemmFp8Args& g, int bn) {
 // CTAs that clusters of `split` fill at once (a GPC's SMs hold whole clusters only)
 template <int BT>
 static int64_t fp8_split_slots(int split) {
-  static int cache[kMaxDevices][9];
+  static DeviceValue slots[9];
   int dev = 0;
-  if (split == 1 || cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return device_sm_count() / split * split;
-  if (cache[dev][split] == 0) {
+  if (split == 1 || cudaGetDevice(&dev) != cudaSuccess) return device_sm_count() / split * split;
+  return slots[split].get(dev, [split] {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)split, 64);
     cfg.blockDim = dim3(192);
@@ -681,9 +681,8 @@ static int64_t fp8_split_slots(int split) {
       cudaGetLastError();
       n = device_sm_count() / (2 * split);  // an estimate that always fits
     }
-    cache[dev][split] = n * split;
-  }
-  return cache[dev][split];
+    return n * split;
+  });
 }
 
 // Best tokens a tile and CTAs a cluster of the split kernel, and its time.

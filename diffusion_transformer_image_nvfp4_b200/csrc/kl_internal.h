@@ -5,11 +5,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kl_host.h"
+
 namespace kl {
 
 constexpr int kNumSMs = 148;  // B200; only caps grid-stride grids (persistent kernels query the device)
 
-int device_sm_count();  // cached per process
+int device_sm_count();  // of the current device
 
 // Launch with programmatic stream serialisation (see pdl_wait / pdl_trigger
 // in kl_common.cuh); every library kernel waits before its first global access.

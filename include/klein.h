@@ -624,8 +624,10 @@ kl_status kl_dit_step_cached(const kl_dit_shape* shape, const kl_dit_weights* w,
  * number of columns, and bf16, fp16 or fp32 elements; pointers need only the
  * alignment of their element type unless stated.  Every size is at least 1
  * (KL_ERR_UNSUPPORTED_SHAPE otherwise).  None of these calls uses a workspace
- * except kl_layer_norm_backward; none keeps anything between calls.  All of
- * them may be captured into a CUDA graph, the first call of a process included.
+ * except kl_layer_norm_backward; none keeps anything of a call for the next (only
+ * facts about a device: its SM count, how many clusters fit).  Host threads may
+ * call at once.  All of them may be captured into a CUDA graph, the first call of
+ * a process included.
  * ---------------------------------------------------------------------- */
 #define KL_BF16 0
 #define KL_F32 1
