@@ -1137,10 +1137,17 @@ static LnShape ln_shape(int64_t cols, int es, bool vec, bool backward) {
 }
 
 // CTAs of a group in the backward pass: enough to fill the GPU, no more than
-// the group has rows for
-static int ln_splits(int64_t groups, int64_t group_rows, const LnShape& sh) {
+// the group has rows for.  Wide rows' parameter sums have CTAs of 256 columns
+// beside: 64 of them a SM (all splits of 16,384 columns) are enough, and the
+// workspace stays below 20 MB or one partial row a group.
+constexpr int64_t kLnWideCtas = 64 * kNumSMs;
+static int ln_splits(int64_t groups, int64_t group_rows, int64_t cols, const LnShape& sh) {
   const int64_t per_sm = sh.tx * sh.ty <= 512 ? 1024 / (sh.tx * sh.ty) : 1;
   int64_t s = (int64_t)kNumSMs * per_sm / groups;
+  if (sh.nv == 0) {
+    const int64_t enough = kLnWideCtas / (groups * ((cols + 255) / 256));
+    if (s > enough) s = enough;
+  }
   const int64_t most = (group_rows + sh.ty - 1) / sh.ty;
   s = s < 1 ? 1 : s;
   return (int)(s < most ? s : most);
@@ -1385,7 +1392,7 @@ size_t kl_layer_norm_backward_workspace_size(int dtype, int64_t rows, int64_t co
   for (int vec = 0; vec < layouts; ++vec) {
     if (ln_few(groups, rows / groups, cols, es, vec != 0)) continue;
     const LnTile t = ln_tile(groups, rows / groups, cols, es, vec != 0);
-    const int s = t.ok ? t.splits : ln_splits(groups, rows / groups, ln_shape(cols, es, vec != 0, true));
+    const int s = t.ok ? t.splits : ln_splits(groups, rows / groups, cols, ln_shape(cols, es, vec != 0, true));
     most = s > most ? s : most;
   }
   return up256((size_t)groups * (size_t)most * 2 * (size_t)cols * sizeof(float));
@@ -1432,7 +1439,7 @@ kl_status kl_layer_norm_backward(const void* dy, int64_t lddy, const void* x, in
   p.dgain = dgain;
   p.dbias = dbias;
   const LnTile tile = ln_tile(groups, p.group_rows, cols, es, vec);
-  p.splits = tile.ok && !few ? tile.splits : ln_splits(groups, p.group_rows, ln_shape(cols, es, vec, true));
+  p.splits = tile.ok && !few ? tile.splits : ln_splits(groups, p.group_rows, cols, ln_shape(cols, es, vec, true));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = dtype == KL_BF16  ? launch_ln_backward<__nv_bfloat16>(p, vec, s)
                   : dtype == KL_F16 ? launch_ln_backward<__half>(p, vec, s)
