@@ -18,8 +18,10 @@
 // reads column pairs of 16 rows and writes 16 contiguous bytes of x^T.
 // B200, device time: rows of bf16 4,608 x 9,216 21.2 us, 20,992 x 3,072 30.8 (91 and
 // 96% of the copy's rate); tiles 20.4 and 29.7 (95 and 99%); transposed rows 30
-// and 44 (64 and 67%, bound by instruction issue; fp32 98%); bf16 rows that no
-// vector load suits, 20,000 x 2,001, 26.6 (52 with single-element loads).
+// and 44 (64 and 67%; fp32 98%), where under the profiler neither DRAM (38%), L1
+// (66%) nor issue (53% of the slots) is full: a CTA loads, waits for its columns'
+// amax and converts in turn, and 43% of the warps are there to hide it; bf16 rows
+// that no vector load suits, 20,000 x 2,001, 26.7 (52 with single-element loads).
 
 #include <type_traits>
 

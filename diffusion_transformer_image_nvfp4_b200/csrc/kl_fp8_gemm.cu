@@ -21,8 +21,10 @@
 //    few and K is long, K is split over a cluster of up to eight CTAs so that
 //    about every SM streams a part of the weights, and the parts' fp32 sums are
 //    added in rank order through distributed shared memory: one launch, no
-//    workspace, the same bits every run.  Bound by HBM at one token (1 x 9,216 x
-//    3,072 in 6.8 us, 8.5 with the weights in HBM: 3.3 TB/s over the launch).
+//    workspace, the same bits every run.  At one token bound by latency and the launch
+//    (1 x 9,216 x 3,072 in 6.8 us, 8.5 with the weights in HBM: 3.3 TB/s over the
+//    launch, half the copy's rate): a CTA asks for the first 10 of its 12 K
+//    blocks at once and for the last two as the first are consumed.
 //
 // Either kernel can take the roles of A and W exchanged (each thread then
 // owns an output column and a warp stores 32 consecutive ones): the split

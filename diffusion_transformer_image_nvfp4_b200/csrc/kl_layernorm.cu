@@ -8,10 +8,15 @@
 //   dgain[c] = sum_r dy * xhat,  dbias[c] = sum_r dy   (rows of the group)
 //
 // mean, rstd and every sum are fp32; the variance is taken about the mean in
-// a second pass over the row in registers, so a large common offset costs
-// nothing.  x (and dy) are read once from memory: both directions are bound by
-// HBM, once their instructions are few enough (packed pairs, parameters staged
-// or held in registers) and their loads far enough ahead.
+// a second pass over the row, so a large common offset does not cancel in it.
+// The mean's own rounding stays: its error times rstd shifts every y of the row.
+// Many rows of up to 768 16-byte vectors (fp32: 1,024 forward, 1,152 backward)
+// are bound by HBM in both directions, once their instructions are few enough
+// (packed pairs, parameters staged or held in registers) and their loads far
+// enough ahead.  x (and dy) are read once from memory up to 4,096 vectors forward
+// and 1,024 backward, off 16 bytes 8,192 and 4,096 columns, the widest a CTA a row
+// and bound by its instructions (72% of the issue slots at 4,096 x 16,384); wider
+// rows are read again for every pass, an element at a time.
 //
 // Forward: a warp a row where there are rows enough, else a CTA a row.
 // Backward: a thread meets the same columns in every row of its CTA, so the
@@ -24,7 +29,10 @@
 // take at the copy's rate); backward 20,992 x 3,072 65.9 us (89% of 59), dx
 // alone 61.7.  Rows that 16-byte vectors do not fit: 4,557 x 2,934 18.8 and 24.1
 // us (two elements at a time; 25.6 and 33.3 with one), 5,000 x 2,047 18.1 and
-// 23.0 (one).
+// 23.0 (one); under the profiler 45 to 47% of the issue slots are busy at 11 to 28%
+// of DRAM: latency and instructions both.  Wide rows, forward and backward: bf16
+// 4,096 x 8,192 55.5 and 66.2, 4,096 x 16,384 81.3 and 435; fp32 4,096 x 5,120
+// 36.0 and 193, 4,096 x 16,384 157 and 449.
 
 #include <type_traits>
 

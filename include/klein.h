@@ -698,8 +698,9 @@ kl_status kl_gemm_fp8_block(const kl_fp8_tensor* A, const kl_fp8_tensor* W, int6
  * copied.  KL_ROPE_INVERSE turns by the negative angle: the inverse, and the
  * gradient with respect to x.  With sections (16, 24, 24), dim 128 and pos =
  * (frame, row, column) the angles are kl_rope_table's for image tokens.
- * Angles are fp64 until they are reduced by whole turns; cos, sin and the
- * rotation are fp32.
+ * Angles are fp64 until they are reduced by whole turns, off by at most 3 * 2^-53
+ * of the position (int64 positions past 2^53 are rounded to fp64); cos, sin and
+ * the rotation are fp32.
  * Strides (batch, token, head) are in elements, dims are consecutive; dim <=
  * 512.  pos: int32, int64 or fp32 [batch, tokens, naxes] consecutive, or
  * [tokens, naxes] for every batch with pos_shared.  out may be x itself with
