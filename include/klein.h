@@ -740,8 +740,9 @@ kl_status kl_rope_axes(const kl_rope_args* args, void* stream);
  * gain / bias [groups, cols] of param_dtype, consecutive: row r uses group
  * r / (rows / groups) (one modulation per image of a batch; groups = 1: shared
  * by all rows; groups must divide rows).  mean, rstd fp32 [rows], NULL if not
- * wanted.  eps >= 0.  The statistics are fp32: where the variance passes its range
- * (a spread of about 1.8e19) rstd is 0, and mean is rounded to it.
+ * wanted.  eps >= 0.  The statistics are fp32 sums: mean is rounded to it, and
+ * where the sum of squares about it passes its range (a spread of about 1.8e19 /
+ * sqrt(cols)) rstd is 0, and so is xhat.
  *
  * kl_layer_norm_backward -- from dy, x and the forward's mean and rstd:
  *   dx = rstd * (h - mean_c(h) - xhat * mean_c(h * xhat)), h = dy * g;
